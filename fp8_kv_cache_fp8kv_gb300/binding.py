@@ -89,6 +89,17 @@ def load(build_if_missing: bool = False):
     lib.fp8kv_paged_prefill_workspace_size.argtypes = [I, I, I, I, I, I, I, I]
     lib.fp8kv_paged_prefill.restype = I
     lib.fp8kv_paged_prefill.argtypes = [P, I64, P, P, I64, P, I, P, P, I, I, I, I, I, I, I, F, F, F, I, P, P, SZ, P]
+    lib.fp8kv_rope_append.restype = I
+    lib.fp8kv_rope_append.argtypes = [P, I64, P, P, I64, P, I64, P, I, P, P, I, I, P, I64, P, P, I64, I, I, I, I, I,
+                                      F, F, P, P, P]
+    lib.fp8kv_rope_append_block.restype = I
+    lib.fp8kv_rope_append_block.argtypes = [P, I64, P, P, I64, P, I64, I64, P, I, P, P, I, I, P, P, P, P, I64, P, I, P,
+                                            P, I, I, I, I, I, I, P, SZ, P]
+    lib.fp8kv_paged_decode_block.restype = I
+    lib.fp8kv_paged_decode_block.argtypes = [P, P, P, P, P, I64, P, I, P, I, I, I, I, I, I, F, I, P, P, SZ, P]
+    lib.fp8kv_paged_prefill_block.restype = I
+    lib.fp8kv_paged_prefill_block.argtypes = [P, I64, P, P, P, P, I64, P, I, P, P, I, I, I, I, I, I, I, F, I, P, P, SZ,
+                                              P]
     _lib = lib
     return lib
 
@@ -508,6 +519,187 @@ def fp8kv_paged_prefill(q, k_cache, v_cache, block_tables, seq_lens, q_starts, m
     q_len tokens over its fp8 cache; see prepare_paged_prefill for shapes."""
     prepare_paged_prefill(q, k_cache, v_cache, block_tables, seq_lens, q_starts, max_q_len, max_seq_len, k_scale,
                           v_scale, sm_scale, window, out, workspace, stream)()
+
+
+# ---------------------------------------------------------------- rotary append, block-scaled cache
+
+# fp8kv_cache_format, fp8kv_rope_style
+CACHE_E4M3, CACHE_E5M2, CACHE_BF16 = 0, 1, 2
+ROPE_HALVES, ROPE_PAIRS = 0, 1
+
+
+def _rows(t, heads, head_dim, name):
+    """(pointer, token stride in elements) of bf16 [T, heads, head_dim] whose
+    tokens may lie apart (a slice of a fused projection's output)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != head_dim):
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    return t.data_ptr(), (st[0] if t.shape[0] > 1 else heads * head_dim)
+
+
+def _same_device(*named):
+    """All tensors on one device, which must be the current one: the library
+    launches on the current device."""
+    dev = torch.cuda.current_device()
+    for name, t in named:
+        if t is not None and t.device.index != dev:
+            raise ValueError("%s is on %s, not on the current device cuda:%d" % (name, t.device, dev))
+
+
+def _rope_args(positions, inv_freq, freq_axis, head_dim, tokens):
+    """(positions, axes, inv_freq, freq_axis, rotary_dim) as the C calls take them."""
+    if inv_freq is None:
+        return None, 1, None, None, 0
+    rotary_dim = 2 * inv_freq.numel()
+    if rotary_dim > head_dim:
+        raise ValueError("inv_freq has more than head_dim / 2 entries")
+    axes = 1
+    if positions is not None:
+        axes = positions.shape[0] if positions.dim() == 2 else 1
+        if positions.dim() not in (1, 2) or positions.shape[-1] != tokens:
+            raise ValueError("positions must be [T] or [axes, T]")
+    if freq_axis is not None and freq_axis.numel() != inv_freq.numel():
+        raise ValueError("freq_axis must have one entry per frequency")
+    return (None if positions is None else _dev(positions, torch.int32, "positions"), axes,
+            _dev(inv_freq, torch.float32, "inv_freq"),
+            None if freq_axis is None else _dev(freq_axis, torch.uint8, "freq_axis"), rotary_dim)
+
+
+def _append_rows(q, k_new, v_new, q_out, hkv, d):
+    """Shapes and pointers of the token rows: (q, q_stride, q_out, k, k_stride, v, v_stride), query heads."""
+    T = k_new.shape[0]
+    if tuple(k_new.shape) != (T, hkv, d) or tuple(v_new.shape) != (T, hkv, d):
+        raise ValueError("k_new/v_new must be [T, Hkv, D] matching the cache")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    hq, qp, qs, qo = 0, None, 0, None
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != d or tuple(q_out.shape) != tuple(q.shape):
+            raise ValueError("q and q_out must be [T, Hq, D]")
+        hq = q.shape[1]
+        qp, qs = _rows(q, hq, d, "q")
+        qo = _dev(q_out, torch.bfloat16, "q_out")
+    return (qp, qs, qo, *_rows(k_new, hkv, d, "k_new"), *_rows(v_new, hkv, d, "v_new")), hq
+
+
+def fp8kv_rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, q_out, k_cache, v_cache, k_scale=1.0,
+                      v_scale=1.0, freq_axis=None, style=ROPE_HALVES, cache_format=CACHE_E4M3, k_scales=None,
+                      v_scales=None, stream=None):
+    """Rotates q [T, Hq, D] into q_out and appends the rotated k_new and v_new
+    [T, Hkv, D] at slot_mapping (int64 [T]); all bf16, tokens may be strided.
+    positions int32 [T] or [axes, T]; inv_freq fp32 [rotary_dim / 2] (None: no
+    rotation); freq_axis uint8, the axis of each frequency.  Caches uint8
+    [num_blocks, Hkv, bs, D] (bf16 for CACHE_BF16).  q and q_out may be None."""
+    nb, hkv, bs, d = k_cache.shape
+    rows, hq = _append_rows(q, k_new, v_new, q_out, hkv, d)
+    T = k_new.shape[0]
+    if tuple(v_cache.shape) != tuple(k_cache.shape) or slot_mapping.numel() != T:
+        raise ValueError("cache or slot_mapping shape mismatch")
+    if (k_scales is not None and k_scales.numel() != hkv) or (v_scales is not None and v_scales.numel() != hkv):
+        raise ValueError("k_scales and v_scales must be [Hkv]")
+    kind = torch.bfloat16 if cache_format == CACHE_BF16 else torch.uint8
+    pos, axes, freq, axis, rotary_dim = _rope_args(positions, inv_freq, freq_axis, d, T)
+    _same_device(("k_new", k_new), ("k_cache", k_cache), ("v_cache", v_cache))
+    code = load().fp8kv_rope_append(
+        *rows, pos, axes, freq, axis, rotary_dim, int(style), _dev(slot_mapping, torch.int64, "slot_mapping"), T,
+        _dev(k_cache, kind, "k_cache"), _dev(v_cache, kind, "v_cache"), nb, bs, hq, hkv, d, int(cache_format),
+        float(k_scale), float(v_scale), None if k_scales is None else _dev(k_scales, torch.float32, "k_scales"),
+        None if v_scales is None else _dev(v_scales, torch.float32, "v_scales"), _stream(stream))
+    _check("fp8kv_rope_append", code)
+
+
+def alloc_append_workspace(device=None, stream=None):
+    """Allocates and zero-fills the error word that fp8kv_rope_append_block
+    needs (any workspace of this library does as well)."""
+    ws = torch.empty(256, dtype=torch.uint8, device=device or "cuda")
+    fp8kv_workspace_init(ws, stream)
+    return ws
+
+
+def _page_scales(k_scales, v_scales, nb, hkv):
+    if tuple(k_scales.shape) != (nb, hkv) or tuple(v_scales.shape) != (nb, hkv):
+        raise ValueError("k_scales and v_scales must be [num_blocks, Hkv]")
+    return _dev(k_scales, torch.float32, "k_scales"), _dev(v_scales, torch.float32, "v_scales")
+
+
+def fp8kv_rope_append_block(q, k_new, v_new, positions, inv_freq, q_out, k_cache, v_cache, k_scales, v_scales,
+                            block_tables, seq_lens, q_starts, max_seq_len, workspace, freq_axis=None,
+                            style=ROPE_HALVES, stream=None):
+    """Rotates q into q_out and appends each sequence's newest rows of k_new
+    (rotated) and v_new to its pages of a block-scaled E4M3 cache; k_scales,
+    v_scales fp32 [num_blocks, Hkv] are updated.  q_starts int32 [B + 1], or
+    None for a decode step (one row per sequence); positions None: each
+    token's place in its sequence.  Other shapes as fp8kv_rope_append and
+    fp8kv_paged_decode."""
+    nb, hkv, bs, d = k_cache.shape
+    rows, hq = _append_rows(q, k_new, v_new, q_out, hkv, d)
+    T, B = k_new.shape[0], seq_lens.numel()
+    if tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("the caches differ in shape")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be [B, max_blocks]")
+    if q_starts is not None and q_starts.numel() != B + 1:
+        raise ValueError("q_starts must be [B + 1]")
+    if q_starts is None and T != B:
+        raise ValueError("without q_starts there is one row per sequence")
+    ks, vs = _page_scales(k_scales, v_scales, nb, hkv)
+    pos, axes, freq, axis, rotary_dim = _rope_args(positions, inv_freq, freq_axis, d, T)
+    _same_device(("k_new", k_new), ("k_cache", k_cache), ("v_cache", v_cache))
+    code = load().fp8kv_rope_append_block(
+        *rows, T, pos, axes, freq, axis, rotary_dim, int(style), _dev(k_cache, torch.uint8, "k_cache"),
+        _dev(v_cache, torch.uint8, "v_cache"), ks, vs, nb, _dev(block_tables, torch.int32, "block_tables"),
+        block_tables.shape[1], _dev(seq_lens, torch.int32, "seq_lens"),
+        None if q_starts is None else _dev(q_starts, torch.int32, "q_starts"), int(max_seq_len), B, hq, hkv, d, bs,
+        _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream))
+    _check("fp8kv_rope_append_block", code)
+
+
+def fp8kv_paged_decode_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, max_seq_len, sm_scale,
+                             window, out, workspace, stream=None):
+    """fp8kv_paged_decode over a block-scaled cache: k_scales, v_scales fp32
+    [num_blocks, Hkv]; other shapes as fp8kv_paged_decode."""
+    B, hq, d = q.shape
+    nb, hkv, bs, d2 = k_cache.shape
+    if d2 != d or tuple(out.shape) != (B, hq, d) or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("shape mismatch between q, out and the caches")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or seq_lens.numel() != B:
+        raise ValueError("block_tables must be [B, max_blocks] and seq_lens [B]")
+    ks, vs = _page_scales(k_scales, v_scales, nb, hkv)
+    _same_device(("q", q), ("k_cache", k_cache), ("v_cache", v_cache))
+    code = load().fp8kv_paged_decode_block(
+        _dev(q, torch.bfloat16, "q"), _dev(k_cache, torch.uint8, "k_cache"), _dev(v_cache, torch.uint8, "v_cache"),
+        ks, vs, nb, _dev(block_tables, torch.int32, "block_tables"), block_tables.shape[1],
+        _dev(seq_lens, torch.int32, "seq_lens"), int(max_seq_len), B, hq, hkv, d, bs, float(sm_scale), int(window),
+        _dev(out, torch.bfloat16, "out"), _dev(workspace, torch.uint8, "workspace"), workspace.numel(),
+        _stream(stream))
+    _check("fp8kv_paged_decode_block", code)
+
+
+def fp8kv_paged_prefill_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, q_starts, max_q_len,
+                              max_seq_len, sm_scale, window, out, workspace, stream=None):
+    """fp8kv_paged_prefill over a block-scaled cache: k_scales, v_scales fp32
+    [num_blocks, Hkv]; other shapes as prepare_paged_prefill."""
+    T, hq, d = q.shape
+    nb, hkv, bs, d2 = k_cache.shape
+    B = seq_lens.numel()
+    if d2 != d or tuple(out.shape) != (T, hq, d) or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("shape mismatch between q, out and the caches")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or q_starts.numel() != B + 1:
+        raise ValueError("block_tables must be [B, max_blocks] and q_starts [B + 1]")
+    ks, vs = _page_scales(k_scales, v_scales, nb, hkv)
+    _same_device(("q", q), ("k_cache", k_cache), ("v_cache", v_cache))
+    code = load().fp8kv_paged_prefill_block(
+        _dev(q, torch.bfloat16, "q"), T, _dev(k_cache, torch.uint8, "k_cache"),
+        _dev(v_cache, torch.uint8, "v_cache"), ks, vs, nb, _dev(block_tables, torch.int32, "block_tables"),
+        block_tables.shape[1], _dev(seq_lens, torch.int32, "seq_lens"), _dev(q_starts, torch.int32, "q_starts"),
+        int(max_q_len), int(max_seq_len), B, hq, hkv, d, bs, float(sm_scale), int(window),
+        _dev(out, torch.bfloat16, "out"), _dev(workspace, torch.uint8, "workspace"), workspace.numel(),
+        _stream(stream))
+    _check("fp8kv_paged_prefill_block", code)
 
 
 # ---------------------------------------------------------------- failure-path test hooks

@@ -1,0 +1,22 @@
+// The streaming decode over a block-scaled E4M3 cache: one K and one V scale
+// for every (page, kv head), the granularity below the per-tensor and per-head
+// scales of gpusmith.com, "FP8 KV Cache Quantization: Capacity Gains and
+// Accuracy Risk", "Scales and calibration".
+//
+// The kernel is stream_decode_kernel (stream_decode.cuh) with BS = true.  With
+// c_t the codes and ks, vs the scales of key t's page,
+//     s_t = sm (q . ck_t) ks,   out = sum_t p_t vs cv_t / sum_t p_t,
+// so the scales cost one multiplication per score (folded into the score
+// multiplier) and one per element of a page's P.V tile.  They are read from
+// HBM with the pages: 8 bytes beside a page's 32 d bytes.
+#include "stream_decode.cuh"
+
+namespace fp8kv {
+
+cudaError_t launch_stream_block(int head_dim, int G, const DecodeArgs& a, int ctas, cudaStream_t s) {
+    return head_dim == 64    ? launch_stream_g<64, 1, false, true>(G, a, ctas, s)
+           : head_dim == 128 ? launch_stream_g<128, 1, false, true>(G, a, ctas, s)
+                             : launch_stream_g<256, 1, false, true>(G, a, ctas, s);
+}
+
+}  // namespace fp8kv

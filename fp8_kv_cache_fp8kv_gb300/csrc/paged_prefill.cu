@@ -81,6 +81,8 @@ struct Args {
     int window;
     float score_scale;           // sm_scale * k_scale * log2(e)
     float v_scale;
+    const float* k_page_scales;  // [num_blocks, Hkv] of a block-scaled cache (the BS kernels; null otherwise)
+    const float* v_page_scales;
     // Failure-path test hook of the tcgen05 kernel (fp8kv_debug_paged_prefill_stall):
     // CTA (0, 0, 0) never issues the score MMAs of stage stall_stage (-1: none),
     // and the MMA waits give up after wait_ns (normally 0.5 s).
@@ -297,7 +299,66 @@ __device__ __forceinline__ void convert_stage(const uint8_t* stg, uint8_t* kt, u
     convert_stage_v<D>(stg, vt, ct, t0, np, kmin, kmax);
 }
 
-template <int D, int G>
+// ---------------------------------------------------------------------------
+// Block scales (BS kernels): one K and one V scale per (page, kv head).
+//
+// With c_t the codes and ks, vs the scales of key t's page (log2 units):
+//     score  s_t = x_t (cs ks),   x_t the raw score q . ck_t,
+//     weight w_t = 2^(s_t + log2 vs - m),
+//     O = sum_t w_t cv_t,   l = sum_t w_t / vs,   out = O / l.
+// The V scale goes into the exponent, where it costs nothing: it is the addend
+// of the FMA that applies the score multiplier, one multiplier and one addend
+// per page of 16 keys.  m is the running maximum of s + log2 vs, so w_t <= 1
+// (or 2^8, see the lazy rescale) however the scales differ, and w_t is rounded
+// to f16 relative to the largest weight in the sum it enters.  The row sum
+// takes each page's weights times 1 / vs, in FP32.
+//
+// The softmax warps fetch their own stage's scales: lane p < PAGES holds page
+// p's, read one stage ahead (the block ids two), and publishes (ks, log2 vs,
+// 1 / vs) to the warp's table in shared memory once a stage.  No other role
+// is involved, so no barrier is added.
+template <int PAGES>
+struct PageScales {
+    const Args& a;
+    const int32_t* bt;   // the sequence's block-table row
+    int hk, end, lane;   // kv head; first page past the range
+    int id;              // block of the page after next's stage, -1: none
+    float k, v;          // next stage's scales
+
+    __device__ __forceinline__ int block_of(int pg) const {
+        int b = -1;
+        if (lane < PAGES && pg + lane < end) {
+            b = __ldg(bt + pg + lane);
+            if (b < 0 || b >= a.num_blocks) b = 0;   // reported by the copies, which read block 0 too
+        }
+        return b;
+    }
+    __device__ __forceinline__ void fetch() {
+        k = v = 1.f;
+        if (id >= 0) {
+            const int64_t at = static_cast<int64_t>(id) * a.num_kv_heads + hk;
+            k = __ldg(a.k_page_scales + at);
+            v = __ldg(a.v_page_scales + at);
+        }
+    }
+    // Starts the reads of the stage at page pg and of the block ids after it.
+    __device__ __forceinline__ PageScales(const Args& args, const int32_t* row, int head, int pg, int past, int ln)
+        : a(args), bt(row), hk(head), end(past), lane(ln) {
+        id = block_of(pg);
+        fetch();
+        id = block_of(pg + PAGES);
+    }
+    // Publishes the scales of the stage at page pg; the reads move on.
+    __device__ __forceinline__ void publish(float4* table, int pg) {
+        __syncwarp();            // the previous stage's entries have been read
+        if (lane < PAGES) table[lane] = make_float4(k, log2f(v), 1.f / v, 0.f);
+        __syncwarp();
+        fetch();
+        id = block_of(pg + 2 * PAGES);
+    }
+};
+
+template <int D, int G, bool BS>
 __global__ void __launch_bounds__(128) paged_prefill_tc_kernel(const Args a) {
     using Tg = TcGeo<D>;
     extern __shared__ uint8_t smem_raw[];
@@ -403,6 +464,8 @@ __global__ void __launch_bounds__(128) paged_prefill_tc_kernel(const Args a) {
         for (int c = 0; c < D / 32; ++c) tc::st32(tm_row + Tg::OACC + 32 * c, z);
         tc::wait_st();
     }
+    __shared__ float4 psc[BS ? kWarps : 1][tcg::kPages];
+    PageScales<BS ? tcg::kPages : 0> feed(a, bt, hk, sp0, sp1, t & 31);
     bool fail = false;
     for (int st = 0; st < nst; ++st) {
         cp_async_wait<0>();            // this stage's copies (this thread's) have landed
@@ -450,7 +513,21 @@ __global__ void __launch_bounds__(128) paged_prefill_tc_kernel(const Args a) {
         tc::wait_ld(*reinterpret_cast<float(*)[32]>(sv + 32));
         const bool interior = np == tcg::kPages && t0 + tcg::kKeys - 1 <= wpos0 && t0 >= wlo1;
         float mx = -INFINITY;
-        if (interior) {
+        if constexpr (BS) {
+            feed.publish(psc[warp], pgs);
+#pragma unroll
+            for (int pp = 0; pp < tcg::kPages; ++pp) {
+                const float4 w = psc[warp][pp];
+                const float c = cs * w.x;
+#pragma unroll
+                for (int i = 0; i < kBS; ++i) {
+                    const int j = pp * kBS + i, key = t0 + j;
+                    const bool valid = interior || (j < np * kBS && rv && key >= lq && key <= pq);
+                    sv[j] = valid ? fmaf(sv[j], c, w.y) : -INFINITY;
+                    mx = fmaxf(mx, sv[j]);
+                }
+            }
+        } else if (interior) {
 #pragma unroll
             for (int j = 0; j < 64; ++j) {
                 sv[j] *= cs;
@@ -469,14 +546,22 @@ __global__ void __launch_bounds__(128) paged_prefill_tc_kernel(const Args a) {
         const float muse = mn == -INFINITY ? 0.f : mn;
         const float alpha = fast_exp2(m - muse);
         m = mn;
-        float ls = 0.f;
+        float ls = 0.f, lpage = 0.f;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             uint32_t pw[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float p0 = fast_exp2(sv[8 * c + 2 * e] - muse), p1 = fast_exp2(sv[8 * c + 2 * e + 1] - muse);
-                ls += p0 + p1;
+                if constexpr (BS) {
+                    lpage += p0 + p1;
+                    if ((c & 1) && e == 3) {   // a page of 16 keys is complete
+                        ls = fmaf(lpage, psc[warp][c >> 1].z, ls);
+                        lpage = 0.f;
+                    }
+                } else {
+                    ls += p0 + p1;
+                }
                 pw[e] = pack_f16x2(p0, p1);
             }
             *reinterpret_cast<uint4*>(sm + Tg::KT + t * 128 + ((c ^ (t & 7)) << 4)) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
@@ -717,7 +802,7 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, ui
     }
 }
 
-template <int D, int G>
+template <int D, int G, bool BS>
 __global__ void __launch_bounds__(ws::kThreads, 1) paged_prefill_ws_kernel(const Args a) {
     using Wg = WsGeo<D>;
     extern __shared__ uint8_t smem_raw[];
@@ -839,9 +924,11 @@ __global__ void __launch_bounds__(ws::kThreads, 1) paged_prefill_ws_kernel(const
     // A pair whose second tile has no rows still runs it (its rows are
     // masked and never stored): skipping the tile's roles measured 10% slower
     // on full pairs, through the branch structure it adds.
+    __shared__ float4 psc[BS ? 8 : 1][ws::kPages];
     float m = -INFINITY, l = 0.f;
     if (warp < 8) {
         // ---------------------------------------------------------- softmax and fold of tile ti
+        PageScales<BS ? ws::kPages : 0> feed(a, bt, hk, sp0, sp1, lane);
         const uint32_t trow = tm + ti * Wg::TC + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         {
             float z[32];
@@ -875,11 +962,29 @@ __global__ void __launch_bounds__(ws::kThreads, 1) paged_prefill_ws_kernel(const
                 return jj < nk && rv && key >= lq && key <= pq;
             };
             float mr[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if constexpr (BS) feed.publish(psc[warp], pgs);
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 float sv[64];
                 load_half(h, sv);
-                if (interior) {
+                if constexpr (BS) {
+                    // page by page: the largest raw score, scaled (cs and the
+                    // K scale are >= 0), plus the V scale's logarithm
+#pragma unroll
+                    for (int pp = 0; pp < 4; ++pp) {
+                        float mp = -INFINITY;
+                        if (interior) {
+#pragma unroll
+                            for (int i = 0; i < kBS; ++i) mp = fmaxf(mp, sv[kBS * pp + i]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < kBS; ++i)
+                                mp = fmaxf(mp, key_ok(64 * h + kBS * pp + i) ? sv[kBS * pp + i] : -INFINITY);
+                        }
+                        const float4 w = psc[warp][4 * h + pp];
+                        if (mp != -INFINITY) mr[pp] = fmaxf(mr[pp], fmaf(mp, cs * w.x, w.y));
+                    }
+                } else if (interior) {
 #pragma unroll
                     for (int j = 0; j < 64; ++j) mr[j & 3] = fmaxf(mr[j & 3], sv[j]);
                 } else {
@@ -888,7 +993,7 @@ __global__ void __launch_bounds__(ws::kThreads, 1) paged_prefill_ws_kernel(const
                 }
             }
             const float mraw = fmaxf(fmaxf(mr[0], mr[1]), fmaxf(mr[2], mr[3]));
-            const float mx = mraw == -INFINITY ? -INFINITY : mraw * cs;
+            const float mx = BS || mraw == -INFINITY ? mraw : mraw * cs;
             // the reference maximum moves only by more than 8 (log2 units);
             // a row that had none (m = -inf) holds O = 0 and l = 0
             const float mn = fmaxf(m, mx);
@@ -921,7 +1026,36 @@ __global__ void __launch_bounds__(ws::kThreads, 1) paged_prefill_ws_kernel(const
                 float sv[64];
                 load_half(h, sv);
                 float pw[32];
-                if (interior) {
+                if constexpr (BS) {
+#pragma unroll
+                    for (int pp = 0; pp < 4; ++pp) {
+                        const float4 w = psc[warp][4 * h + pp];
+                        const float c = cs * w.x, n = w.y + nmuse;
+                        float ps[2] = {0.f, 0.f};
+                        if (interior) {
+#pragma unroll
+                            for (int i = 0; i < kBS / 2; ++i) {   // key pairs in packed FP32 pairs
+                                const int j = kBS / 2 * pp + i;
+                                float x0, x1;
+                                fma_f32x2(x0, x1, sv[2 * j], sv[2 * j + 1], c, c, n, n);
+                                const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                                add_f32x2(ps[0], ps[1], p0, p1);
+                                pw[j] = __uint_as_float(pack_f16x2(p0, p1));
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < kBS / 2; ++i) {   // masked keys weigh 0
+                                const int j = kBS / 2 * pp + i;
+                                const float p0 = key_ok(64 * h + 2 * j) ? fast_exp2(fmaf(sv[2 * j], c, n)) : 0.f;
+                                const float p1 = key_ok(64 * h + 2 * j + 1) ? fast_exp2(fmaf(sv[2 * j + 1], c, n)) : 0.f;
+                                ps[0] += p0;
+                                ps[1] += p1;
+                                pw[j] = __uint_as_float(pack_f16x2(p0, p1));
+                            }
+                        }
+                        lp[pp] = fmaf(ps[0] + ps[1], w.z, lp[pp]);
+                    }
+                } else if (interior) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {   // key pairs in packed FP32 pairs
                         float x0, x1;
@@ -1123,7 +1257,7 @@ struct Ws1Geo {
     static_assert(D == 64 || D == 256, "the one-tile warp-specialised kernel covers d = 64 and 256");
 };
 
-template <int D, int G>
+template <int D, int G, bool BS>
 __global__ void __launch_bounds__(ws1::kThreads, Ws1Geo<D>::kCtasPerSm) paged_prefill_ws1_kernel(const Args a) {
     using namespace ws1;
     using Wg = Ws1Geo<D>;
@@ -1223,9 +1357,11 @@ __global__ void __launch_bounds__(ws1::kThreads, Ws1Geo<D>::kCtasPerSm) paged_pr
     tc::fence_after_sync();
     const uint32_t tm = tmem_base;
 
+    __shared__ float4 psc[BS ? 4 : 1][tcg::kPages];
     float m = -INFINITY, l = 0.f;
     if (warp < 4) {
         // ---------------------------------------------------------- softmax and fold
+        PageScales<BS ? tcg::kPages : 0> feed(a, bt, hk, sp0, sp1, lane);
         const uint32_t trow = tm + (static_cast<uint32_t>(warp * 32) << 16);
         {
             float z[32];
@@ -1255,7 +1391,23 @@ __global__ void __launch_bounds__(ws1::kThreads, Ws1Geo<D>::kCtasPerSm) paged_pr
                 return j < np * kBS && rv && key >= lq && key <= pq;
             };
             float mr[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            if (interior) {
+            if constexpr (BS) {
+                feed.publish(psc[warp], pgs);
+#pragma unroll
+                for (int pp = 0; pp < tcg::kPages; ++pp) {
+                    float mp = -INFINITY;
+                    if (interior) {
+#pragma unroll
+                        for (int i = 0; i < kBS; ++i) mp = fmaxf(mp, sv[kBS * pp + i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kBS; ++i)
+                            mp = fmaxf(mp, key_ok(kBS * pp + i) ? sv[kBS * pp + i] : -INFINITY);
+                    }
+                    const float4 w = psc[warp][pp];
+                    if (mp != -INFINITY) mr[pp] = fmaf(mp, cs * w.x, w.y);
+                }
+            } else if (interior) {
 #pragma unroll
                 for (int j = 0; j < 64; ++j) mr[j & 3] = fmaxf(mr[j & 3], sv[j]);
             } else {
@@ -1263,7 +1415,7 @@ __global__ void __launch_bounds__(ws1::kThreads, Ws1Geo<D>::kCtasPerSm) paged_pr
                 for (int j = 0; j < 64; ++j) mr[j & 3] = fmaxf(mr[j & 3], key_ok(j) ? sv[j] : -INFINITY);
             }
             const float mraw = fmaxf(fmaxf(mr[0], mr[1]), fmaxf(mr[2], mr[3]));
-            const float mx = mraw == -INFINITY ? -INFINITY : mraw * cs;
+            const float mx = BS || mraw == -INFINITY ? mraw : mraw * cs;
             const float mn = fmaxf(m, mx);
             const float muse = mn == -INFINITY ? 0.f : mn;
             const float alpha = fast_exp2(m - muse);
@@ -1271,6 +1423,7 @@ __global__ void __launch_bounds__(ws1::kThreads, Ws1Geo<D>::kCtasPerSm) paged_pr
             float lp[4] = {0.f, 0.f, 0.f, 0.f};
             // pof(j, p0, p1): the weights of keys j and j + 1
             auto emit = [&](auto pof) {
+                [[maybe_unused]] float ps[2] = {0.f, 0.f};    // BS: the weights of the page so far
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     uint32_t pw[4];
@@ -1278,13 +1431,43 @@ __global__ void __launch_bounds__(ws1::kThreads, Ws1Geo<D>::kCtasPerSm) paged_pr
                     for (int e = 0; e < 4; ++e) {
                         float p0, p1;
                         pof(8 * c + 2 * e, p0, p1);
-                        add_f32x2(lp[2 * (e & 1)], lp[2 * (e & 1) + 1], p0, p1);
+                        if constexpr (BS) add_f32x2(ps[0], ps[1], p0, p1);
+                        else add_f32x2(lp[2 * (e & 1)], lp[2 * (e & 1) + 1], p0, p1);
                         pw[e] = pack_f16x2(p0, p1);
+                    }
+                    if constexpr (BS) {
+                        if (c & 1) {         // a page of 16 keys is complete
+                            lp[c >> 1] = (ps[0] + ps[1]) * psc[warp][c >> 1].z;
+                            ps[0] = ps[1] = 0.f;
+                        }
                     }
                     *reinterpret_cast<uint4*>(prow + ((c ^ (tid & 7)) << 4)) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
                 }
             };
-            if (interior) {
+            if constexpr (BS) {
+                float c[tcg::kPages], n[tcg::kPages];
+#pragma unroll
+                for (int pp = 0; pp < tcg::kPages; ++pp) {
+                    const float4 w = psc[warp][pp];
+                    c[pp] = cs * w.x;
+                    n[pp] = w.y - muse;
+                }
+                if (interior) {
+                    emit([&](int j, float& p0, float& p1) {
+                        float x0, x1;
+                        const float cc = c[j / kBS], nn = n[j / kBS];
+                        fma_f32x2(x0, x1, sv[j], sv[j + 1], cc, cc, nn, nn);
+                        p0 = fast_exp2(x0);
+                        p1 = fast_exp2(x1);
+                    });
+                } else {
+                    emit([&](int j, float& p0, float& p1) {
+                        const float cc = c[j / kBS], nn = n[j / kBS];
+                        p0 = key_ok(j) ? fast_exp2(fmaf(sv[j], cc, nn)) : 0.f;
+                        p1 = key_ok(j + 1) ? fast_exp2(fmaf(sv[j + 1], cc, nn)) : 0.f;
+                    });
+                }
+            } else if (interior) {
                 emit([&](int j, float& p0, float& p1) {   // key pairs in packed FP32 pairs
                     float x0, x1;
                     fma_f32x2(x0, x1, sv[j], sv[j + 1], cs, cs, -muse, -muse);
@@ -1576,37 +1759,35 @@ Plan make_plan(int batch, int max_q_len, int max_seq_len, int G, int Hkv, int D,
 
 // The prefill kernel of a kind (kernel_kind) for (D, G), its dynamic shared
 // memory and its threads.
-template <int D, int G>
+template <int D, int G, bool BS>
 void kernel_of(int kind, void (**fn)(const Args), size_t* smem, int* threads) {
     if constexpr (D == 64 || D == 128) {
         if (kind == 1) {
-            *fn = paged_prefill_ws_kernel<D, G>;
+            *fn = paged_prefill_ws_kernel<D, G, BS>;
             *smem = static_cast<size_t>(WsGeo<D>::SMEM) + 1024;
             *threads = ws::kThreads;
             return;
         }
     }
-    if constexpr (D == 256) {
-        if (kind == 2) {
-            *fn = paged_prefill_ws1_kernel<D, G>;
-            *smem = static_cast<size_t>(Ws1Geo<D>::SMEM) + 1024;
-            *threads = ws1::kThreads;
-            return;
-        }
+    if constexpr (D == 256) {   // kind 2 always
+        *fn = paged_prefill_ws1_kernel<D, G, BS>;
+        *smem = static_cast<size_t>(Ws1Geo<D>::SMEM) + 1024;
+        *threads = ws1::kThreads;
+    } else {
+        *fn = paged_prefill_tc_kernel<D, G, BS>;
+        *smem = static_cast<size_t>(TcGeo<D>::SMEM) + 1024;
+        *threads = kThreads;
     }
-    *fn = paged_prefill_tc_kernel<D, G>;
-    *smem = static_cast<size_t>(TcGeo<D>::SMEM) + 1024;
-    *threads = kThreads;
 }
 
 template <int D>
 bool kernel_of_g(int G, int kind, void (**fn)(const Args), size_t* smem, int* threads) {
     switch (G) {
-        case 1: kernel_of<D, 1>(kind, fn, smem, threads); return true;
-        case 2: kernel_of<D, 2>(kind, fn, smem, threads); return true;
-        case 4: kernel_of<D, 4>(kind, fn, smem, threads); return true;
-        case 8: kernel_of<D, 8>(kind, fn, smem, threads); return true;
-        case 16: kernel_of<D, 16>(kind, fn, smem, threads); return true;
+        case 1: kernel_of<D, 1, false>(kind, fn, smem, threads); return true;
+        case 2: kernel_of<D, 2, false>(kind, fn, smem, threads); return true;
+        case 4: kernel_of<D, 4, false>(kind, fn, smem, threads); return true;
+        case 8: kernel_of<D, 8, false>(kind, fn, smem, threads); return true;
+        case 16: kernel_of<D, 16, false>(kind, fn, smem, threads); return true;
         default: return false;
     }
 }
@@ -1640,13 +1821,13 @@ int resident_per_sm(int D, int G, int kind) {
     return n;
 }
 
-template <int D, int G>
+template <int D, int G, bool BS>
 cudaError_t launch(const Args& a, int batch, cudaStream_t s) {
     const int kind = kernel_kind(D, a.tiles);
     void (*kernel)(const Args) = nullptr;
     size_t smem = 0;
     int threads = 0;
-    kernel_of<D, G>(kind, &kernel, &smem, &threads);
+    kernel_of<D, G, BS>(kind, &kernel, &smem, &threads);
     static std::atomic<uint64_t> done_mask[3] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1681,14 +1862,14 @@ cudaError_t launch(const Args& a, int batch, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, prefill_merge_kernel<D, G>, a);
 }
 
-template <int D>
+template <int D, bool BS>
 cudaError_t launch_g(int G, const Args& a, int batch, cudaStream_t s) {
     switch (G) {
-        case 1: return launch<D, 1>(a, batch, s);
-        case 2: return launch<D, 2>(a, batch, s);
-        case 4: return launch<D, 4>(a, batch, s);
-        case 8: return launch<D, 8>(a, batch, s);
-        case 16: return launch<D, 16>(a, batch, s);
+        case 1: return launch<D, 1, BS>(a, batch, s);
+        case 2: return launch<D, 2, BS>(a, batch, s);
+        case 4: return launch<D, 4, BS>(a, batch, s);
+        case 8: return launch<D, 8, BS>(a, batch, s);
+        case 16: return launch<D, 16, BS>(a, batch, s);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -1732,7 +1913,8 @@ fp8kv_status prefill_impl(const void* q, int64_t num_q_tokens, const uint8_t* k_
                           const int32_t* seq_lens, const int32_t* q_starts, int max_q_len, int max_seq_len, int batch,
                           int num_q_heads, int num_kv_heads, int head_dim, int block_size, float k_scale,
                           float v_scale, float sm_scale, int window, void* out, void* workspace,
-                          size_t workspace_bytes, void* stream, int stall_stage, uint64_t wait_ns) {
+                          size_t workspace_bytes, void* stream, int stall_stage, uint64_t wait_ns,
+                          const float* k_page_scales = nullptr, const float* v_page_scales = nullptr) {
     using namespace fp8kv::prefill;
     auto a16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
     const fp8kv_status sh = check_shape(batch, max_q_len, max_seq_len, num_q_heads, num_kv_heads, head_dim,
@@ -1785,14 +1967,17 @@ fp8kv_status prefill_impl(const void* q, int64_t num_q_tokens, const uint8_t* k_
     a.window = window > 0 ? window : 0;
     a.score_scale = sm_scale * k_scale * kLog2e;
     a.v_scale = v_scale;
+    a.k_page_scales = k_page_scales;
+    a.v_page_scales = v_page_scales;
     a.wait_ns = wait_ns;
     a.stall_stage = stall_stage;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
+    const bool bs = k_page_scales != nullptr;
     switch (head_dim) {
-        case 64: e = launch_g<64>(G, a, batch, s); break;
-        case 128: e = launch_g<128>(G, a, batch, s); break;
-        default: e = launch_g<256>(G, a, batch, s); break;
+        case 64: e = bs ? launch_g<64, true>(G, a, batch, s) : launch_g<64, false>(G, a, batch, s); break;
+        case 128: e = bs ? launch_g<128, true>(G, a, batch, s) : launch_g<128, false>(G, a, batch, s); break;
+        default: e = bs ? launch_g<256, true>(G, a, batch, s) : launch_g<256, false>(G, a, batch, s); break;
     }
     return e == cudaSuccess ? FP8KV_OK : FP8KV_ERR_CUDA;
 }
@@ -1811,6 +1996,25 @@ extern "C" fp8kv_status fp8kv_paged_prefill(const void* q, int64_t num_q_tokens,
                         q_starts, max_q_len, max_seq_len, batch, num_q_heads, num_kv_heads, head_dim, block_size,
                         k_scale, v_scale, sm_scale, window, out, workspace, workspace_bytes, stream, -1,
                         fp8kv::prefill::tcg::kWaitNs);
+}
+
+extern "C" fp8kv_status fp8kv_paged_prefill_block(const void* q, int64_t num_q_tokens, const uint8_t* k_cache,
+                                                  const uint8_t* v_cache, const float* k_scales,
+                                                  const float* v_scales, int64_t num_blocks,
+                                                  const int32_t* block_tables, int max_blocks_per_seq,
+                                                  const int32_t* seq_lens, const int32_t* q_starts, int max_q_len,
+                                                  int max_seq_len, int batch, int num_q_heads, int num_kv_heads,
+                                                  int head_dim, int block_size, float sm_scale, int window, void* out,
+                                                  void* workspace, size_t workspace_bytes, void* stream) {
+    FP8KV_TRACE("fp8kv_paged_prefill_block");
+    if (batch > 0 && max_q_len > 0 && num_q_tokens > 0 &&
+        (!k_scales || !v_scales || (reinterpret_cast<uintptr_t>(k_scales) & 3u) ||
+         (reinterpret_cast<uintptr_t>(v_scales) & 3u)))
+        return FP8KV_ERR_INVALID_ARG;
+    return prefill_impl(q, num_q_tokens, k_cache, v_cache, num_blocks, block_tables, max_blocks_per_seq, seq_lens,
+                        q_starts, max_q_len, max_seq_len, batch, num_q_heads, num_kv_heads, head_dim, block_size, 1.f,
+                        1.f, sm_scale, window, out, workspace, workspace_bytes, stream, -1,
+                        fp8kv::prefill::tcg::kWaitNs, k_scales, v_scales);
 }
 
 extern "C" fp8kv_status fp8kv_debug_paged_prefill_stall(

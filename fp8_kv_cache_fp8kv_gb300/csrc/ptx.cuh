@@ -99,6 +99,11 @@ __device__ __forceinline__ void cp_async_16(uint32_t smem_dst, const void* src) 
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(src) : "memory");
 }
 
+// The same for 4 bytes, 4-byte aligned (through L1: cp.async.cg copies 16 bytes only).
+__device__ __forceinline__ void cp_async_4(uint32_t smem_dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_dst), "l"(src) : "memory");
+}
+
 // Closes the calling thread's current group of cp.async copies.
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 

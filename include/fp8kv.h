@@ -425,6 +425,167 @@ fp8kv_status fp8kv_paged_prefill(const void* q, int64_t num_q_tokens, const uint
                                  float v_scale, float sm_scale, int window, void* out, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
+/* What a cache page holds (fp8kv_rope_append). */
+typedef enum {
+    FP8KV_CACHE_E4M3 = 0, /* the cache of fp8kv_quant_append, fp8kv_paged_decode, fp8kv_paged_prefill */
+    FP8KV_CACHE_E5M2 = 1, /* the cache of fp8kv_quant_append_e5m2 and fp8kv_paged_decode_e5m2         */
+    FP8KV_CACHE_BF16 = 2  /* the cache of fp8kv_paged_decode_bf16                                     */
+} fp8kv_cache_format;
+
+/* Which elements of a head a rotation pairs, R = rotary_dim. */
+typedef enum {
+    FP8KV_ROPE_HALVES = 0, /* frequency i turns elements i and i + R/2  */
+    FP8KV_ROPE_PAIRS = 1   /* frequency i turns elements 2i and 2i + 1  */
+} fp8kv_rope_style;
+
+/*
+ * Rotary positions on the way into the cache: q rotated into q_out, k rotated,
+ * k and v quantised and written through a slot mapping.  No counterpart on the
+ * pages, which start from rotated keys; it stands in front of every decode
+ * and prefill call of this library.
+ *
+ * For token t and frequency i < rotary_dim / 2:
+ *     angle = positions[axis(i)][t] * inv_freq[i]
+ * as a real product (the kernels keep it to about 2^-48 of its size before
+ * the fraction of a turn is taken, so positions of 2^20 lose nothing), and the pair (x, y) the
+ * frequency owns (fp8kv_rope_style) becomes
+ *     (x cos - y sin, y cos + x sin)
+ * in fp32.  Elements from rotary_dim on pass unchanged.  q_out is rounded once
+ * to bf16 (RNE).  k is not rounded before its conversion, which together with
+ * v's is that of fp8kv_quant_append (E4M3: one fp32 division by the scale, one
+ * RNE saturating conversion), fp8kv_quant_append_e5m2, or bf16 RNE.  With
+ * rotary_dim 0 the cache bytes are exactly theirs.
+ *
+ *   q, q_out       bf16; token t's heads at q + t * q_stride elements, q_out
+ *                  contiguous [num_tokens][num_q_heads][head_dim].  Both null:
+ *                  no queries.  q_out may be q itself if q is contiguous; any
+ *                  other overlap is undefined.
+ *   k_new, v_new   bf16; token t's heads at k_new + t * k_stride elements.
+ *                  Slices of one fused projection's output fit: the strides
+ *                  are multiples of 8 and at least a row, the pointers
+ *                  16-byte aligned.
+ *   positions      int32 [num_axes][num_tokens]; num_axes 1..4.  One axis for
+ *                  text; time, height and width for images and video.
+ *   inv_freq       fp32 [rotary_dim / 2]
+ *   freq_axis      uint8 [rotary_dim / 2], the axis of each frequency (in runs
+ *                  or interleaved, as the model has them); null: axis 0.  A
+ *                  value outside [0, num_axes) is read as axis 0.
+ *   rotary_dim     0 (positions, inv_freq and freq_axis unused) or a multiple
+ *                  of 16 up to head_dim
+ *   slot_mapping   int64 [num_tokens], 8-byte aligned, as fp8kv_quant_append: a
+ *                  negative or out-of-range slot skips the token's cache
+ *                  write; its query is rotated all the same.  A slot given to
+ *                  two tokens gets one of their rows, or a mix.
+ *   k_cache,       [num_blocks][num_kv_heads][block_size][head_dim] of
+ *   v_cache        cache_format, 16-byte aligned
+ *   k_scale,       per-tensor scales, finite and > 0 (1 for a bf16 cache);
+ *   v_scale        not used where k_scales, v_scales are given
+ *   k_scales,      DEVICE fp32 [num_kv_heads] as fp8kv_quant_append_per_head,
+ *   v_scales       or both null (null for a bf16 cache)
+ * All of positions, inv_freq, freq_axis, slot_mapping, k_scales and v_scales
+ * are device pointers.
+ * Supported: head_dim in {64, 128, 256}; block_size >= 1; num_tokens < 2^31.
+ * num_tokens == 0 is a no-op.
+ */
+fp8kv_status fp8kv_rope_append(const void* q, int64_t q_stride, void* q_out, const void* k_new, int64_t k_stride,
+                               const void* v_new, int64_t v_stride, const int32_t* positions, int num_axes,
+                               const float* inv_freq, const uint8_t* freq_axis, int rotary_dim, int rope_style,
+                               const int64_t* slot_mapping, int64_t num_tokens, void* k_cache, void* v_cache,
+                               int64_t num_blocks, int block_size, int num_q_heads, int num_kv_heads, int head_dim,
+                               int cache_format, float k_scale, float v_scale, const float* k_scales,
+                               const float* v_scales, void* stream);
+
+/*
+ * The block-scaled cache: E4M3 codes with one scale for each (page, kv head)
+ * of K and one of V [below the granularities of G "Scales and calibration"].
+ * No calibration: the append chooses the scales from the rows it writes.
+ *
+ *   k_scales, v_scales  DEVICE fp32 [num_blocks][num_kv_heads], 4-byte
+ *                       aligned.  They may be the append's or the caller's
+ *                       own (a page filled elsewhere).  Finite and within
+ *                       [2^-40, 2^40] for every page that is attended or
+ *                       appended to behind older rows; other values give
+ *                       unspecified codes and outputs (not checked on the
+ *                       device).  Need no initialisation: a page whose first
+ *                       row is appended gets its scale then.
+ *
+ * fp8kv_rope_append_block rotates q and k as fp8kv_rope_append and appends
+ * the newest n = q_starts[b+1] - q_starts[b] tokens of every sequence (of its
+ * seq_lens[b], they included) to its pages.  For each page, kv head and each
+ * of K (rotated) and V, with amax the largest finite magnitude of the new rows:
+ *   - the page holds older rows of the sequence, and amax <= 448 * s for its
+ *     scale s: the scale stays, the new rows are written under it;
+ *   - otherwise the scale becomes 2^e (or stays, if larger), e the least whole
+ *     number in [-40, 40] with amax <= 448 * 2^e, and the older rows' codes c
+ *     become E4M3(decode(c) * (s_old / s_new)).
+ * New codes are E4M3(x / s): one fp32 division, one RNE saturating conversion
+ * (infinities saturate, NaN stays NaN; neither takes part in amax).
+ *
+ *   q .. rope_style     as fp8kv_rope_append; tokens packed by sequence
+ *   num_tokens          rows of q, k_new, v_new and positions
+ *   positions           null with num_axes 1: each token's place in its sequence
+ *   block_tables        int32 [batch][max_blocks_per_seq], as fp8kv_paged_decode.
+ *                       The pages written must belong to one sequence each:
+ *                       a page that two sequences append to in one call gets
+ *                       unspecified codes and scales.
+ *   seq_lens            int32 [batch] on the device
+ *   q_starts            int32 [batch + 1] on the device, non-decreasing, or
+ *                       null: a decode step, row b is sequence b's newest token
+ *                       (num_tokens == batch; seq_lens[b] == 0 skips the row).
+ *                       Rows of q_out outside [q_starts[0], q_starts[batch])
+ *                       are left as they are.
+ *   workspace           256-byte aligned, at least 256 bytes, zero-filled before
+ *                       first use (fp8kv_workspace_init): the error word that
+ *                       fp8kv_read_error reads.  Any workspace of this library
+ *                       will do, in the order its calls share it.  Reported as
+ *                       FP8KV_ERR_INVALID_ARG: a block id outside
+ *                       [0, num_blocks) (the page is not written, its queries
+ *                       are rotated), and a sequence whose seq_lens or q_starts
+ *                       do not satisfy 0 <= n <= seq_lens[b] <= max_seq_len
+ *                       and q_starts[b+1] <= num_tokens (it is skipped).
+ * Supported: head_dim in {64, 128, 256}; block_size == 16; batch <= 65535;
+ *            num_blocks * num_kv_heads < 2^31; num_tokens < 2^31.  batch == 0,
+ *            num_tokens == 0 or max_seq_len == 0 is a no-op.
+ */
+fp8kv_status fp8kv_rope_append_block(const void* q, int64_t q_stride, void* q_out, const void* k_new,
+                                     int64_t k_stride, const void* v_new, int64_t v_stride, int64_t num_tokens,
+                                     const int32_t* positions, int num_axes, const float* inv_freq,
+                                     const uint8_t* freq_axis, int rotary_dim, int rope_style, uint8_t* k_cache,
+                                     uint8_t* v_cache, float* k_scales, float* v_scales, int64_t num_blocks,
+                                     const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                     const int32_t* q_starts, int max_seq_len, int batch, int num_q_heads,
+                                     int num_kv_heads, int head_dim, int block_size, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/*
+ * fp8kv_paged_decode over a block-scaled cache: key t's code stands for
+ * decode(code) * k_scales[page(t)][hk], value t's for decode(code) *
+ * v_scales[page(t)][hk].  Scores are scaled page by page in FP32; each page's
+ * P.V tile is multiplied by its V scale as it is added into the FP32
+ * accumulators, so pages of very different scales do not cost one another
+ * precision.  All other arguments, the workspace
+ * (fp8kv_paged_decode_workspace_size) and the errors as fp8kv_paged_decode.
+ */
+fp8kv_status fp8kv_paged_decode_block(const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                                      const float* k_scales, const float* v_scales, int64_t num_blocks,
+                                      const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                      int max_seq_len, int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                                      int block_size, float sm_scale, int window, void* out, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/*
+ * fp8kv_paged_prefill over a block-scaled cache (append the chunk first, with
+ * fp8kv_rope_append_block).  All other arguments, the workspace
+ * (fp8kv_paged_prefill_workspace_size) and the errors as fp8kv_paged_prefill.
+ */
+fp8kv_status fp8kv_paged_prefill_block(const void* q, int64_t num_q_tokens, const uint8_t* k_cache,
+                                       const uint8_t* v_cache, const float* k_scales, const float* v_scales,
+                                       int64_t num_blocks, const int32_t* block_tables, int max_blocks_per_seq,
+                                       const int32_t* seq_lens, const int32_t* q_starts, int max_q_len,
+                                       int max_seq_len, int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                                       int block_size, float sm_scale, int window, void* out, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
 /*
  * Failure-path test hooks.  No counterpart on the pages: the pages' failure
  * mode is silent (a wrong answer, no error), and these make the library's

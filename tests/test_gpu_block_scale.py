@@ -1,0 +1,219 @@
+"""GPU tests of attention over the block-scaled cache: decode and prefill
+against the fp64 oracle, element by element within the roundings' bound."""
+import numpy as np
+import pytest
+import torch
+
+from fp8_kv_cache_fp8kv_gb300 import binding as fk
+from oracle import rope_block as rb
+from tests.block_harness import Cache, check_rows, f64, randn, run_decode, run_prefill
+
+pytestmark = pytest.mark.gpu
+
+LAYOUTS = [(32, 8, 128), (64, 8, 64), (8, 1, 256), (4, 4, 128), (3, 3, 64), (4, 2, 256), (16, 1, 64), (16, 1, 128),
+           (16, 1, 256)]
+
+
+def _decode_case(c, hq, sm, window, seed, **kw):
+    q = randn((len(c.lens), hq, c.d), seed + 1)
+    out = f64(run_decode(c, q.cuda(), sm, window, **kw))
+    for b, L in enumerate(c.lens):
+        if L == 0:
+            assert not out[b].any()
+        else:
+            check_rows(out[b:b + 1], c, b, f64(q[b:b + 1]), [L - 1], sm, window, False, "sequence %d of %d" % (b, L))
+
+
+@pytest.mark.parametrize("hq,hkv,d", LAYOUTS)
+def test_decode_layouts_and_lengths(hq, hkv, d):
+    c = Cache(hkv, d, [1, 0, 15, 16, 17, 33, 500, 2049, 0], seed=hq + d).cuda()
+    _decode_case(c, hq, d ** -0.5, 0, hq)
+
+
+@pytest.mark.parametrize("window", [1, 15, 16, 17, 100, 4000])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (16, 2, 64), (8, 1, 256)])
+def test_decode_windows(hq, hkv, d, window):
+    c = Cache(hkv, d, [1, 16, 17, 100, 101, 0, 1500], seed=window).cuda()
+    _decode_case(c, hq, d ** -0.5, window, window)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (16, 2, 64), (8, 1, 256), (16, 1, 128)])
+@pytest.mark.parametrize("exponent", [0, 30, -30])
+def test_scales_that_differ_by_2_to_the_40(hq, hkv, d, exponent):
+    """Neighbouring pages 2^40 apart: the small ones count as exactly where the large ones weigh little."""
+    c = Cache(hkv, d, [400, 37], seed=5, spread=0.0, scale=2.0 ** -7)
+    sign = np.where(np.arange(c.nb) % 2, 1.0, -1.0)[:, None]
+    c.vs = (c.vs * 2.0 ** (min(max(exponent, -12), 12) + 20 * sign)).astype(np.float32)
+    c.ks = (c.ks * 2.0 ** np.random.default_rng(1).uniform(-20, 0, c.ks.shape)).astype(np.float32)
+    c.cuda()
+    _decode_case(c, hq, d ** -0.5, 0, 3)
+    _prefill_case(c, hq, [9, 37], d ** -0.5, 0, 4)
+
+
+def test_small_value_pages_survive_beside_large_ones():
+    """All the probability on a page whose V scale is 2^-20 of its neighbour's: the answer is that page's values, to
+    the accuracy of its own scale, and not lost in the neighbour's."""
+    hq, hkv, d = 4, 1, 128
+    c = Cache(hkv, d, [32], seed=8, spread=0.0)
+    a, z = c.tables[0, :2]
+    c.k[:] = 0
+    c.k[a, 0, 3] = 0x70                    # the one key that every query meets: codes of 128
+    c.vs[a], c.vs[z] = 2.0 ** -18, 2.0 ** 2
+    c.cuda()
+    q = torch.ones((1, hq, d), dtype=torch.bfloat16)
+    out = f64(run_decode(c, q.cuda(), 1.0))
+    want = rb.values(c.v, c.vs, c.tables[0], 32)[3, 0]
+    assert np.abs(out[0] - want).max() <= 2.0 ** -8 * np.abs(want).max()
+    out = f64(run_prefill(c, q.cuda(), torch.tensor([0, 1], dtype=torch.int32).cuda(), 1, 1.0))
+    assert np.abs(out[0] - want).max() <= 2.0 ** -8 * np.abs(want).max()
+
+
+def test_zero_value_sink_keeps_its_weight():
+    """A first page of zero values with the least scale still takes its share of the softmax."""
+    for hq, hkv, d in ((4, 1, 128), (8, 1, 64), (4, 1, 256)):
+        c = Cache(hkv, d, [300], seed=2)
+        a = c.tables[0, 0]
+        c.v[a], c.vs[a] = 0, 2.0 ** -40
+        c.ks[a] *= 3
+        c.cuda()
+        _decode_case(c, hq, d ** -0.5, 0, 1)
+        _prefill_case(c, hq, [200], d ** -0.5, 0, 1)
+
+
+@pytest.mark.parametrize("sm", [0.0, -0.1, 30.0])
+def test_score_scales(sm):
+    for hq, hkv, d in ((8, 2, 128), (8, 1, 64), (8, 1, 256)):
+        c = Cache(hkv, d, [70, 200], seed=4, scale=0.003).cuda()
+        q = randn((2, hq, d), 9, 0.1)
+        out = f64(run_decode(c, q.cuda(), sm))
+        for b in range(2):
+            check_rows(out[b:b + 1], c, b, f64(q[b:b + 1]), [c.lens[b] - 1], sm, 0, False)
+        _prefill_case(c, hq, [70, 45], sm, 0, 9, qscale=0.1)
+
+
+def test_decode_more_sequences_than_one_launch():
+    c = Cache(1, 64, [(37 * i) % 60 for i in range(520)], seed=6).cuda()
+    _decode_case(c, 4, 0.125, 0, 2)
+
+
+def test_decode_long_context_split_over_the_grid():
+    for hq, hkv, d, L in ((32, 4, 128, 40000), (8, 1, 256, 20000), (64, 4, 64, 20000)):
+        c = Cache(hkv, d, [L], seed=7).cuda()
+        _decode_case(c, hq, d ** -0.5, 0, 3)
+
+
+def _prefill_case(c, hq, counts, sm, window, seed, qscale=1.0):
+    starts = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    q = randn((int(starts[-1]), hq, c.d), seed + 1, qscale)
+    out = f64(run_prefill(c, q.cuda(), torch.from_numpy(starts).cuda(), max(counts), sm, window))
+    for b, n in enumerate(counts):
+        L = c.lens[b]
+        check_rows(out[starts[b]:starts[b + 1]], c, b, f64(q[starts[b]:starts[b + 1]]), list(range(L - n, L)), sm,
+                   window, True, "sequence %d: %d of %d" % (b, n, L))
+
+
+@pytest.mark.parametrize("hq,hkv,d", LAYOUTS)
+def test_prefill_layouts(hq, hkv, d):
+    c = Cache(hkv, d, [1, 0, 17, 40, 200, 333], seed=hq + d).cuda()
+    _prefill_case(c, hq, [1, 0, 17, 3, 70, 33], d ** -0.5, 0, 1)
+    _prefill_case(c, hq, [1, 0, 1, 1, 1, 1], d ** -0.5, 0, 2)     # one query tile a sequence
+
+
+@pytest.mark.parametrize("window", [1, 16, 40, 5000])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (16, 2, 64), (4, 1, 256)])
+def test_prefill_windows(hq, hkv, d, window):
+    c = Cache(hkv, d, [17, 300, 200], seed=window).cuda()
+    _prefill_case(c, hq, [17, 90, 5], d ** -0.5, window, 1)
+    _prefill_case(c, hq, [2, 1, 3], d ** -0.5, window, 2)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (16, 2, 64), (4, 1, 256)])
+def test_prefill_splits_a_long_context(hq, hkv, d):
+    c = Cache(hkv, d, [5000, 777], seed=1).cuda()
+    _prefill_case(c, hq, [5, 2], d ** -0.5, 0, 1)
+    _prefill_case(c, hq, [40, 20], d ** -0.5, 0, 2)
+
+
+def test_prefill_rows_are_the_decode_of_their_prefix():
+    """The last row of a chunk and the decode of the same sequence agree within both bounds."""
+    c = Cache(8, 128, [1000], seed=3).cuda()
+    q = randn((1, 32, 128), 5).cuda()
+    a = f64(run_decode(c, q, 128 ** -0.5))
+    b = f64(run_prefill(c, q, torch.tensor([0, 1], dtype=torch.int32).cuda(), 1, 128 ** -0.5))
+    assert np.abs(a - b).max() <= 2 * 2.0 ** -8 * np.abs(a).max()
+
+
+def test_bad_block_ids_are_reported_and_read_as_block_0():
+    for d, hq in ((128, 8), (64, 8), (256, 8)):
+        c = Cache(2, d, [100, 60], seed=2).cuda()
+        c.gt[0, 2] = c.nb
+        c.gt[1, 1] = -7
+        c.gks[0], c.gvs[0] = 0.01, 0.01            # block 0 may be one that no sequence owns
+        c.gk[0], c.gv[0] = 0x30, 0x30
+        ws = fk.alloc_workspace(2, hq, 2, d, 100)
+        out = run_decode(c, randn((2, hq, d), 1).cuda(), 0.1, ws=ws)
+        torch.cuda.synchronize()
+        assert fk.fp8kv_read_error(ws) == 1 and torch.isfinite(out).all()
+        for counts in ([3, 2], [90, 60]):
+            ws = fk.alloc_prefill_workspace(2, max(counts), 100, hq, 2, d)
+            starts = torch.tensor([0, counts[0], sum(counts)], dtype=torch.int32).cuda()
+            out = run_prefill(c, randn((sum(counts), hq, d), 1).cuda(), starts, max(counts), 0.1, ws=ws)
+            torch.cuda.synchronize()
+            assert fk.fp8kv_read_error(ws) == 1 and torch.isfinite(out).all()
+
+
+def test_captured_and_replayed_on_another_stream():
+    c = Cache(8, 128, [300, 77, 0], seed=9).cuda()
+    q = randn((3, 32, 128), 1).cuda()
+    starts = torch.tensor([0, 40, 45, 45], dtype=torch.int32).cuda()
+    qp = randn((45, 32, 128), 2).cuda()
+    ws = fk.alloc_workspace(3, 32, 8, 128, 300)
+    wsp = fk.alloc_prefill_workspace(3, 40, 300, 32, 8, 128)
+    out, outp = torch.zeros_like(q), torch.zeros_like(qp)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        run_decode(c, q, 0.1, ws=ws, out=out)
+        run_prefill(c, qp, starts, 40, 0.1, ws=wsp, out=outp)
+    st.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        run_decode(c, q, 0.1, ws=ws, out=out)
+        run_prefill(c, qp, starts, 40, 0.1, ws=wsp, out=outp)
+    q.copy_(randn((3, 32, 128), 3))
+    qp.copy_(randn((45, 32, 128), 4))
+    c.gvs *= 2                                    # the scales are read at replay
+    c.pull()
+    for _ in range(3):
+        out.zero_(), outp.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        check_rows(f64(out[:1]), c, 0, f64(q[:1]), [299], 0.1, 0, False)
+        check_rows(f64(out[1:2]), c, 1, f64(q[1:2]), [76], 0.1, 0, False)
+        assert not out[2].any()
+        check_rows(f64(outp[:40]), c, 0, f64(qp[:40]), list(range(260, 300)), 0.1, 0, True)
+        check_rows(f64(outp[40:]), c, 1, f64(qp[40:]), list(range(72, 77)), 0.1, 0, True)
+    assert fk.fp8kv_read_error(ws) == 0 and fk.fp8kv_read_error(wsp) == 0
+
+
+def test_cache_offsets_past_32_bits():
+    """Pages behind the first 4 GiB of each cache."""
+    hq, hkv, d = 32, 8, 128
+    small = Cache(hkv, d, [100, 40], seed=3)
+    nb = (1 << 32) // (hkv * 16 * d) + 64
+    shift = nb - small.nb
+    big_k = torch.empty((nb, hkv, 16, d), dtype=torch.uint8, device="cuda")
+    big_v = torch.empty_like(big_k)
+    ks, vs = (torch.full((nb, hkv), float("nan"), device="cuda") for _ in range(2))
+    small.cuda()
+    big_k[shift:], big_v[shift:], ks[shift:], vs[shift:] = small.gk, small.gv, small.gks, small.gvs
+    q = randn((2, hq, d), 1)
+    qp, starts = randn((30, hq, d), 2), torch.tensor([0, 20, 30], dtype=torch.int32).cuda()
+    small.gk, small.gv, small.gks, small.gvs = big_k, big_v, ks, vs
+    small.gt = torch.from_numpy(np.where(small.tables < small.nb, small.tables + shift, 0).astype(np.int32)).cuda()
+    out = f64(run_decode(small, q.cuda(), 0.1))
+    outp = f64(run_prefill(small, qp.cuda(), starts, 20, 0.1))
+    for b, L in enumerate(small.lens):
+        check_rows(out[b:b + 1], small, b, f64(q[b:b + 1]), [L - 1], 0.1, 0, False)
+    check_rows(outp[:20], small, 0, f64(qp[:20]), list(range(80, 100)), 0.1, 0, True)
+    check_rows(outp[20:], small, 1, f64(qp[20:]), list(range(30, 40)), 0.1, 0, True)
