@@ -522,68 +522,91 @@ def fp8kv_paged_prefill(q, k_cache, v_cache, block_tables, seq_lens, q_starts, m
 
 
 # ---------------------------------------------------------------- rotary append, block-scaled cache
+#
+# A decode step calls these once a layer, on kernels of 5 to 60 us, so their
+# checks are written for the host's time: one test of what can be wrong with a
+# tensor, the reason worked out only where it fails.
 
 # fp8kv_cache_format, fp8kv_rope_style
 CACHE_E4M3, CACHE_E5M2, CACHE_BF16 = 0, 1, 2
 ROPE_HALVES, ROPE_PAIRS = 0, 1
 
+_BF16, _U8, _I32, _F32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
 
-def _rows(t, heads, head_dim, name):
+
+def _ptr(t, dtype, dev, name):
+    """Device pointer of a contiguous CUDA tensor on device `dev` (the current
+    one: the library launches on it)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    _dev(t, dtype, name)
+    raise ValueError("%s is on %s, not on the current device cuda:%d" % (name, t.device, dev))
+
+
+def _opt(t, dtype, dev, name):
+    return None if t is None else _ptr(t, dtype, dev, name)
+
+
+def _rows(t, heads, head_dim, dev, name):
     """(pointer, token stride in elements) of bf16 [T, heads, head_dim] whose
     tokens may lie apart (a slice of a fused projection's output)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype != torch.bfloat16:
-        raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
+    if t.dtype is not _BF16:
+        raise TypeError("%s must be %s, got %s" % (name, _BF16, t.dtype))
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s, not on the current device cuda:%d" % (name, t.device, dev))
     st = t.stride()
     if st[2] != 1 or (heads > 1 and st[1] != head_dim):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
     return t.data_ptr(), (st[0] if t.shape[0] > 1 else heads * head_dim)
 
 
-def _same_device(*named):
-    """All tensors on one device, which must be the current one: the library
-    launches on the current device."""
-    dev = torch.cuda.current_device()
-    for name, t in named:
-        if t is not None and t.device.index != dev:
-            raise ValueError("%s is on %s, not on the current device cuda:%d" % (name, t.device, dev))
+def _where(stream, cache):
+    """(current device, the stream's handle): the given stream, or the current one of that device."""
+    if not isinstance(cache, torch.Tensor) or not cache.is_cuda:
+        raise TypeError("k_cache must be a CUDA tensor")
+    dev = torch._C._cuda_getDevice()
+    return dev, (torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
 
 
-def _rope_args(positions, inv_freq, freq_axis, head_dim, tokens):
+def _rope_args(positions, inv_freq, freq_axis, head_dim, tokens, dev):
     """(positions, axes, inv_freq, freq_axis, rotary_dim) as the C calls take them."""
     if inv_freq is None:
         return None, 1, None, None, 0
-    rotary_dim = 2 * inv_freq.numel()
-    if rotary_dim > head_dim:
+    half = inv_freq.numel()
+    if 2 * half > head_dim:
         raise ValueError("inv_freq has more than head_dim / 2 entries")
     axes = 1
     if positions is not None:
-        axes = positions.shape[0] if positions.dim() == 2 else 1
-        if positions.dim() not in (1, 2) or positions.shape[-1] != tokens:
+        shape = positions.shape
+        axes = shape[0] if len(shape) == 2 else 1
+        if len(shape) not in (1, 2) or shape[-1] != tokens:
             raise ValueError("positions must be [T] or [axes, T]")
-    if freq_axis is not None and freq_axis.numel() != inv_freq.numel():
+    if freq_axis is not None and freq_axis.numel() != half:
         raise ValueError("freq_axis must have one entry per frequency")
-    return (None if positions is None else _dev(positions, torch.int32, "positions"), axes,
-            _dev(inv_freq, torch.float32, "inv_freq"),
-            None if freq_axis is None else _dev(freq_axis, torch.uint8, "freq_axis"), rotary_dim)
+    return (_opt(positions, _I32, dev, "positions"), axes, _ptr(inv_freq, _F32, dev, "inv_freq"),
+            _opt(freq_axis, _U8, dev, "freq_axis"), 2 * half)
 
 
-def _append_rows(q, k_new, v_new, q_out, hkv, d):
+def _append_rows(q, k_new, v_new, q_out, hkv, d, dev):
     """Shapes and pointers of the token rows: (q, q_stride, q_out, k, k_stride, v, v_stride), query heads."""
-    T = k_new.shape[0]
-    if tuple(k_new.shape) != (T, hkv, d) or tuple(v_new.shape) != (T, hkv, d):
+    shape = k_new.shape
+    if len(shape) != 3 or shape[1] != hkv or shape[2] != d or v_new.shape != shape:
         raise ValueError("k_new/v_new must be [T, Hkv, D] matching the cache")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out come together")
     hq, qp, qs, qo = 0, None, 0, None
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != d or tuple(q_out.shape) != tuple(q.shape):
+        qshape = q.shape
+        if len(qshape) != 3 or qshape[0] != shape[0] or qshape[2] != d or q_out.shape != qshape:
             raise ValueError("q and q_out must be [T, Hq, D]")
-        hq = q.shape[1]
-        qp, qs = _rows(q, hq, d, "q")
-        qo = _dev(q_out, torch.bfloat16, "q_out")
-    return (qp, qs, qo, *_rows(k_new, hkv, d, "k_new"), *_rows(v_new, hkv, d, "v_new")), hq
+        hq = qshape[1]
+        qp, qs = _rows(q, hq, d, dev, "q")
+        qo = _ptr(q_out, _BF16, dev, "q_out")
+    kp, ks = _rows(k_new, hkv, d, dev, "k_new")
+    vp, vs = _rows(v_new, hkv, d, dev, "v_new")
+    return (qp, qs, qo, kp, ks, vp, vs), hq
 
 
 def fp8kv_rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, q_out, k_cache, v_cache, k_scale=1.0,
@@ -595,21 +618,22 @@ def fp8kv_rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, q_out,
     rotation); freq_axis uint8, the axis of each frequency.  Caches uint8
     [num_blocks, Hkv, bs, D] (bf16 for CACHE_BF16).  q and q_out may be None."""
     nb, hkv, bs, d = k_cache.shape
-    rows, hq = _append_rows(q, k_new, v_new, q_out, hkv, d)
+    dev, st = _where(stream, k_cache)
+    rows, hq = _append_rows(q, k_new, v_new, q_out, hkv, d, dev)
     T = k_new.shape[0]
-    if tuple(v_cache.shape) != tuple(k_cache.shape) or slot_mapping.numel() != T:
+    if v_cache.shape != k_cache.shape or slot_mapping.numel() != T:
         raise ValueError("cache or slot_mapping shape mismatch")
     if (k_scales is not None and k_scales.numel() != hkv) or (v_scales is not None and v_scales.numel() != hkv):
         raise ValueError("k_scales and v_scales must be [Hkv]")
-    kind = torch.bfloat16 if cache_format == CACHE_BF16 else torch.uint8
-    pos, axes, freq, axis, rotary_dim = _rope_args(positions, inv_freq, freq_axis, d, T)
-    _same_device(("k_new", k_new), ("k_cache", k_cache), ("v_cache", v_cache))
+    kind = _BF16 if cache_format == CACHE_BF16 else _U8
+    rope = _rope_args(positions, inv_freq, freq_axis, d, T, dev)
     code = load().fp8kv_rope_append(
-        *rows, pos, axes, freq, axis, rotary_dim, int(style), _dev(slot_mapping, torch.int64, "slot_mapping"), T,
-        _dev(k_cache, kind, "k_cache"), _dev(v_cache, kind, "v_cache"), nb, bs, hq, hkv, d, int(cache_format),
-        float(k_scale), float(v_scale), None if k_scales is None else _dev(k_scales, torch.float32, "k_scales"),
-        None if v_scales is None else _dev(v_scales, torch.float32, "v_scales"), _stream(stream))
-    _check("fp8kv_rope_append", code)
+        *rows, *rope, int(style), _ptr(slot_mapping, torch.int64, dev, "slot_mapping"), T,
+        _ptr(k_cache, kind, dev, "k_cache"), _ptr(v_cache, kind, dev, "v_cache"), nb, bs, hq, hkv, d,
+        int(cache_format), float(k_scale), float(v_scale), _opt(k_scales, _F32, dev, "k_scales"),
+        _opt(v_scales, _F32, dev, "v_scales"), st)
+    if code:
+        raise Fp8kvError("fp8kv_rope_append", code)
 
 
 def alloc_append_workspace(device=None, stream=None):
@@ -620,10 +644,21 @@ def alloc_append_workspace(device=None, stream=None):
     return ws
 
 
-def _page_scales(k_scales, v_scales, nb, hkv):
-    if tuple(k_scales.shape) != (nb, hkv) or tuple(v_scales.shape) != (nb, hkv):
+def _block_shapes(k_cache, v_cache, k_scales, v_scales, block_tables, batch):
+    shape, want = k_cache.shape, k_cache.shape[:2]
+    if v_cache.shape != shape:
+        raise ValueError("the caches differ in shape")
+    if k_scales.shape != want or v_scales.shape != want:
         raise ValueError("k_scales and v_scales must be [num_blocks, Hkv]")
-    return _dev(k_scales, torch.float32, "k_scales"), _dev(v_scales, torch.float32, "v_scales")
+    shape = block_tables.shape
+    if len(shape) != 2 or shape[0] != batch:
+        raise ValueError("block_tables must be [B, max_blocks]")
+    return shape[1]
+
+
+def _block_ptrs(k_cache, v_cache, k_scales, v_scales, dev):
+    return (_ptr(k_cache, _U8, dev, "k_cache"), _ptr(v_cache, _U8, dev, "v_cache"),
+            _ptr(k_scales, _F32, dev, "k_scales"), _ptr(v_scales, _F32, dev, "v_scales"))
 
 
 def fp8kv_rope_append_block(q, k_new, v_new, positions, inv_freq, q_out, k_cache, v_cache, k_scales, v_scales,
@@ -636,26 +671,23 @@ def fp8kv_rope_append_block(q, k_new, v_new, positions, inv_freq, q_out, k_cache
     token's place in its sequence.  Other shapes as fp8kv_rope_append and
     fp8kv_paged_decode."""
     nb, hkv, bs, d = k_cache.shape
-    rows, hq = _append_rows(q, k_new, v_new, q_out, hkv, d)
     T, B = k_new.shape[0], seq_lens.numel()
-    if tuple(v_cache.shape) != tuple(k_cache.shape):
-        raise ValueError("the caches differ in shape")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B:
-        raise ValueError("block_tables must be [B, max_blocks]")
-    if q_starts is not None and q_starts.numel() != B + 1:
+    mb = _block_shapes(k_cache, v_cache, k_scales, v_scales, block_tables, B)
+    dev, st = _where(stream, k_cache)
+    rows, hq = _append_rows(q, k_new, v_new, q_out, hkv, d, dev)
+    if q_starts is None:
+        if T != B:
+            raise ValueError("without q_starts there is one row per sequence")
+    elif q_starts.numel() != B + 1:
         raise ValueError("q_starts must be [B + 1]")
-    if q_starts is None and T != B:
-        raise ValueError("without q_starts there is one row per sequence")
-    ks, vs = _page_scales(k_scales, v_scales, nb, hkv)
-    pos, axes, freq, axis, rotary_dim = _rope_args(positions, inv_freq, freq_axis, d, T)
-    _same_device(("k_new", k_new), ("k_cache", k_cache), ("v_cache", v_cache))
+    rope = _rope_args(positions, inv_freq, freq_axis, d, T, dev)
     code = load().fp8kv_rope_append_block(
-        *rows, T, pos, axes, freq, axis, rotary_dim, int(style), _dev(k_cache, torch.uint8, "k_cache"),
-        _dev(v_cache, torch.uint8, "v_cache"), ks, vs, nb, _dev(block_tables, torch.int32, "block_tables"),
-        block_tables.shape[1], _dev(seq_lens, torch.int32, "seq_lens"),
-        None if q_starts is None else _dev(q_starts, torch.int32, "q_starts"), int(max_seq_len), B, hq, hkv, d, bs,
-        _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream))
-    _check("fp8kv_rope_append_block", code)
+        *rows, T, *rope, int(style), *_block_ptrs(k_cache, v_cache, k_scales, v_scales, dev), nb,
+        _ptr(block_tables, _I32, dev, "block_tables"), mb, _ptr(seq_lens, _I32, dev, "seq_lens"),
+        _opt(q_starts, _I32, dev, "q_starts"), int(max_seq_len), B, hq, hkv, d, bs,
+        _ptr(workspace, _U8, dev, "workspace"), workspace.numel(), st)
+    if code:
+        raise Fp8kvError("fp8kv_rope_append_block", code)
 
 
 def fp8kv_paged_decode_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, max_seq_len, sm_scale,
@@ -664,19 +696,19 @@ def fp8kv_paged_decode_block(q, k_cache, v_cache, k_scales, v_scales, block_tabl
     [num_blocks, Hkv]; other shapes as fp8kv_paged_decode."""
     B, hq, d = q.shape
     nb, hkv, bs, d2 = k_cache.shape
-    if d2 != d or tuple(out.shape) != (B, hq, d) or tuple(v_cache.shape) != tuple(k_cache.shape):
+    if d2 != d or out.shape != q.shape:
         raise ValueError("shape mismatch between q, out and the caches")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or seq_lens.numel() != B:
-        raise ValueError("block_tables must be [B, max_blocks] and seq_lens [B]")
-    ks, vs = _page_scales(k_scales, v_scales, nb, hkv)
-    _same_device(("q", q), ("k_cache", k_cache), ("v_cache", v_cache))
+    if seq_lens.numel() != B:
+        raise ValueError("seq_lens must be [B]")
+    mb = _block_shapes(k_cache, v_cache, k_scales, v_scales, block_tables, B)
+    dev, st = _where(stream, k_cache)
     code = load().fp8kv_paged_decode_block(
-        _dev(q, torch.bfloat16, "q"), _dev(k_cache, torch.uint8, "k_cache"), _dev(v_cache, torch.uint8, "v_cache"),
-        ks, vs, nb, _dev(block_tables, torch.int32, "block_tables"), block_tables.shape[1],
-        _dev(seq_lens, torch.int32, "seq_lens"), int(max_seq_len), B, hq, hkv, d, bs, float(sm_scale), int(window),
-        _dev(out, torch.bfloat16, "out"), _dev(workspace, torch.uint8, "workspace"), workspace.numel(),
-        _stream(stream))
-    _check("fp8kv_paged_decode_block", code)
+        _ptr(q, _BF16, dev, "q"), *_block_ptrs(k_cache, v_cache, k_scales, v_scales, dev), nb,
+        _ptr(block_tables, _I32, dev, "block_tables"), mb, _ptr(seq_lens, _I32, dev, "seq_lens"), int(max_seq_len), B,
+        hq, hkv, d, bs, float(sm_scale), int(window), _ptr(out, _BF16, dev, "out"), _ptr(workspace, _U8, dev, "workspace"),
+        workspace.numel(), st)
+    if code:
+        raise Fp8kvError("fp8kv_paged_decode_block", code)
 
 
 def fp8kv_paged_prefill_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, q_starts, max_q_len,
@@ -686,20 +718,20 @@ def fp8kv_paged_prefill_block(q, k_cache, v_cache, k_scales, v_scales, block_tab
     T, hq, d = q.shape
     nb, hkv, bs, d2 = k_cache.shape
     B = seq_lens.numel()
-    if d2 != d or tuple(out.shape) != (T, hq, d) or tuple(v_cache.shape) != tuple(k_cache.shape):
+    if d2 != d or out.shape != q.shape:
         raise ValueError("shape mismatch between q, out and the caches")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or q_starts.numel() != B + 1:
-        raise ValueError("block_tables must be [B, max_blocks] and q_starts [B + 1]")
-    ks, vs = _page_scales(k_scales, v_scales, nb, hkv)
-    _same_device(("q", q), ("k_cache", k_cache), ("v_cache", v_cache))
+    if q_starts.numel() != B + 1:
+        raise ValueError("q_starts must be [B + 1]")
+    mb = _block_shapes(k_cache, v_cache, k_scales, v_scales, block_tables, B)
+    dev, st = _where(stream, k_cache)
     code = load().fp8kv_paged_prefill_block(
-        _dev(q, torch.bfloat16, "q"), T, _dev(k_cache, torch.uint8, "k_cache"),
-        _dev(v_cache, torch.uint8, "v_cache"), ks, vs, nb, _dev(block_tables, torch.int32, "block_tables"),
-        block_tables.shape[1], _dev(seq_lens, torch.int32, "seq_lens"), _dev(q_starts, torch.int32, "q_starts"),
-        int(max_q_len), int(max_seq_len), B, hq, hkv, d, bs, float(sm_scale), int(window),
-        _dev(out, torch.bfloat16, "out"), _dev(workspace, torch.uint8, "workspace"), workspace.numel(),
-        _stream(stream))
-    _check("fp8kv_paged_prefill_block", code)
+        _ptr(q, _BF16, dev, "q"), T, *_block_ptrs(k_cache, v_cache, k_scales, v_scales, dev), nb,
+        _ptr(block_tables, _I32, dev, "block_tables"), mb, _ptr(seq_lens, _I32, dev, "seq_lens"),
+        _ptr(q_starts, _I32, dev, "q_starts"), int(max_q_len), int(max_seq_len), B, hq, hkv, d, bs,
+        float(sm_scale), int(window), _ptr(out, _BF16, dev, "out"), _ptr(workspace, _U8, dev, "workspace"),
+        workspace.numel(), st)
+    if code:
+        raise Fp8kvError("fp8kv_paged_prefill_block", code)
 
 
 # ---------------------------------------------------------------- failure-path test hooks

@@ -154,13 +154,13 @@ def test_appends_refuse_mismatched_shapes(kw, block):
 
 def test_rope_arguments_are_checked():
     f = fk._rope_args
-    assert f(None, None, None, 64, 6)[4] == 0
+    assert f(None, None, None, 64, 6, 0)[4] == 0
     for bad in (dict(positions=_i32(5)), dict(positions=_i32(2, 5)), dict(positions=_i32(1, 2, 6)),
                 dict(inv_freq=torch.zeros(33)), dict(freq_axis=torch.zeros(31, dtype=torch.uint8))):
         a = dict(positions=None, inv_freq=torch.zeros(32), freq_axis=None)
         a.update(bad)
         with pytest.raises(ValueError):
-            f(a["positions"], a["inv_freq"], a["freq_axis"], 64, 6)
+            f(a["positions"], a["inv_freq"], a["freq_axis"], 64, 6, 0)
 
 
 def test_host_tensors_are_refused():
