@@ -100,6 +100,8 @@ def load(build_if_missing: bool = False):
     lib.fp8kv_paged_prefill_block.restype = I
     lib.fp8kv_paged_prefill_block.argtypes = [P, I64, P, P, P, P, I64, P, I, P, P, I, I, I, I, I, I, I, F, I, P, P, SZ,
                                               P]
+    lib.fp8kv_debug_paged_prefill_block_stall.restype = I
+    lib.fp8kv_debug_paged_prefill_block_stall.argtypes = lib.fp8kv_paged_prefill_block.argtypes + [I, U64]
     _lib = lib
     return lib
 
@@ -705,16 +707,14 @@ def fp8kv_paged_decode_block(q, k_cache, v_cache, k_scales, v_scales, block_tabl
     code = load().fp8kv_paged_decode_block(
         _ptr(q, _BF16, dev, "q"), *_block_ptrs(k_cache, v_cache, k_scales, v_scales, dev), nb,
         _ptr(block_tables, _I32, dev, "block_tables"), mb, _ptr(seq_lens, _I32, dev, "seq_lens"), int(max_seq_len), B,
-        hq, hkv, d, bs, float(sm_scale), int(window), _ptr(out, _BF16, dev, "out"), _ptr(workspace, _U8, dev, "workspace"),
-        workspace.numel(), st)
+        hq, hkv, d, bs, float(sm_scale), int(window), _ptr(out, _BF16, dev, "out"),
+        _ptr(workspace, _U8, dev, "workspace"), workspace.numel(), st)
     if code:
         raise Fp8kvError("fp8kv_paged_decode_block", code)
 
 
-def fp8kv_paged_prefill_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, q_starts, max_q_len,
-                              max_seq_len, sm_scale, window, out, workspace, stream=None):
-    """fp8kv_paged_prefill over a block-scaled cache: k_scales, v_scales fp32
-    [num_blocks, Hkv]; other shapes as prepare_paged_prefill."""
+def _prefill_block_args(q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, q_starts, max_q_len,
+                        max_seq_len, sm_scale, window, out, workspace, stream):
     T, hq, d = q.shape
     nb, hkv, bs, d2 = k_cache.shape
     B = seq_lens.numel()
@@ -724,12 +724,20 @@ def fp8kv_paged_prefill_block(q, k_cache, v_cache, k_scales, v_scales, block_tab
         raise ValueError("q_starts must be [B + 1]")
     mb = _block_shapes(k_cache, v_cache, k_scales, v_scales, block_tables, B)
     dev, st = _where(stream, k_cache)
-    code = load().fp8kv_paged_prefill_block(
-        _ptr(q, _BF16, dev, "q"), T, *_block_ptrs(k_cache, v_cache, k_scales, v_scales, dev), nb,
-        _ptr(block_tables, _I32, dev, "block_tables"), mb, _ptr(seq_lens, _I32, dev, "seq_lens"),
-        _ptr(q_starts, _I32, dev, "q_starts"), int(max_q_len), int(max_seq_len), B, hq, hkv, d, bs,
-        float(sm_scale), int(window), _ptr(out, _BF16, dev, "out"), _ptr(workspace, _U8, dev, "workspace"),
-        workspace.numel(), st)
+    return (_ptr(q, _BF16, dev, "q"), T, *_block_ptrs(k_cache, v_cache, k_scales, v_scales, dev), nb,
+            _ptr(block_tables, _I32, dev, "block_tables"), mb, _ptr(seq_lens, _I32, dev, "seq_lens"),
+            _ptr(q_starts, _I32, dev, "q_starts"), int(max_q_len), int(max_seq_len), B, hq, hkv, d, bs,
+            float(sm_scale), int(window), _ptr(out, _BF16, dev, "out"), _ptr(workspace, _U8, dev, "workspace"),
+            workspace.numel(), st)
+
+
+def fp8kv_paged_prefill_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, q_starts, max_q_len,
+                              max_seq_len, sm_scale, window, out, workspace, stream=None):
+    """fp8kv_paged_prefill over a block-scaled cache: k_scales, v_scales fp32
+    [num_blocks, Hkv]; other shapes as prepare_paged_prefill."""
+    code = load().fp8kv_paged_prefill_block(*_prefill_block_args(
+        q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, q_starts, max_q_len, max_seq_len, sm_scale,
+        window, out, workspace, stream))
     if code:
         raise Fp8kvError("fp8kv_paged_prefill_block", code)
 
@@ -756,3 +764,12 @@ def debug_paged_prefill_stall(q, k_cache, v_cache, block_tables, seq_lens, q_sta
     args = prepare_paged_prefill(q, k_cache, v_cache, block_tables, seq_lens, q_starts, max_q_len, max_seq_len,
                                  k_scale, v_scale, sm_scale, window, out, workspace, stream).args
     return load().fp8kv_debug_paged_prefill_stall(*args, ctypes.c_int(stall_stage), ctypes.c_uint64(wait_limit_ns))
+
+
+def debug_paged_prefill_block_stall(q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, q_starts,
+                                    max_q_len, max_seq_len, sm_scale, window, out, workspace, stall_stage,
+                                    wait_limit_ns, stream=None) -> int:
+    """The same for fp8kv_paged_prefill_block."""
+    return load().fp8kv_debug_paged_prefill_block_stall(*_prefill_block_args(
+        q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, q_starts, max_q_len, max_seq_len, sm_scale,
+        window, out, workspace, stream), int(stall_stage), int(wait_limit_ns))

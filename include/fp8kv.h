@@ -412,7 +412,7 @@ fp8kv_status fp8kv_paged_decode_noalloc(const void* q, const uint8_t* k_cache, c
  * device: the key-range split plan depends on its SM count and on how many
  * prefill CTAs it holds at once.  At least 256 (the error word); larger
  * when the call splits key ranges.  Returns 0 if the arguments are invalid
- * or no device is available.
+ * or no device is available.  Enough for fp8kv_paged_prefill_block too.
  */
 size_t fp8kv_paged_prefill_workspace_size(int batch, int max_q_len, int max_seq_len, int num_q_heads,
                                           int num_kv_heads, int head_dim, int block_size, int window);
@@ -625,6 +625,14 @@ fp8kv_status fp8kv_debug_paged_prefill_stall(const void* q, int64_t num_q_tokens
                                              float sm_scale, int window, void* out, void* workspace,
                                              size_t workspace_bytes, void* stream, int stall_stage,
                                              uint64_t wait_limit_ns);
+
+/* The same hook for fp8kv_paged_prefill_block. */
+fp8kv_status fp8kv_debug_paged_prefill_block_stall(
+    const void* q, int64_t num_q_tokens, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scales,
+    const float* v_scales, int64_t num_blocks, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* seq_lens, const int32_t* q_starts, int max_q_len, int max_seq_len, int batch, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, float sm_scale, int window, void* out, void* workspace,
+    size_t workspace_bytes, void* stream, int stall_stage, uint64_t wait_limit_ns);
 
 #ifdef __cplusplus
 }

@@ -217,3 +217,53 @@ def test_cache_offsets_past_32_bits():
         check_rows(out[b:b + 1], small, b, f64(q[b:b + 1]), [L - 1], 0.1, 0, False)
     check_rows(outp[:20], small, 0, f64(qp[:20]), list(range(80, 100)), 0.1, 0, True)
     check_rows(outp[20:], small, 1, f64(qp[20:]), list(range(30, 40)), 0.1, 0, True)
+
+
+@pytest.mark.parametrize("L,stage", [(1500, 0), (20000, 1)])   # CTA 0's part of 1500 keys is one stage
+@pytest.mark.parametrize("hq,hkv,d,n", [(8, 2, 128, 5), (8, 2, 128, 30), (8, 2, 64, 8), (8, 1, 256, 60),
+                                        (16, 2, 128, 100)])
+def test_a_wait_that_runs_out_is_reported_and_ends_the_call(hq, hkv, d, n, L, stage):
+    """One stage's scores never arrive: every role gives up, and after fp8kv_workspace_init the call is right again."""
+    c = Cache(hkv, d, [L], seed=4).cuda()
+    q = randn((n, hq, d), 1).cuda()
+    starts = torch.tensor([0, n], dtype=torch.int32).cuda()
+    ws = fk.alloc_prefill_workspace(1, n, L, hq, hkv, d)
+    out = torch.full_like(q, 7.0)
+    assert fk.debug_paged_prefill_block_stall(q, c.gk, c.gv, c.gks, c.gvs, c.gt, c.gl, starts, n, L, 0.1, 0, out, ws,
+                                              stage, 2_000_000) == 0
+    torch.cuda.synchronize()
+    assert fk.fp8kv_read_error(ws) == 5
+    fk.fp8kv_workspace_init(ws)
+    run_prefill(c, q, starts, n, 0.1, ws=ws, out=out)
+    torch.cuda.synchronize()
+    assert fk.fp8kv_read_error(ws) == 0
+    check_rows(f64(out), c, 0, f64(q), list(range(L - n, L)), 0.1, 0, True)
+
+
+@pytest.mark.parametrize("hq,hkv,d,n", [(4, 1, 128, 8), (4, 1, 128, 16), (4, 1, 128, 17), (4, 1, 128, 32), (4, 1, 128, 33),
+                                        (8, 1, 64, 4), (8, 1, 64, 8), (8, 1, 64, 16), (8, 1, 64, 17), (8, 1, 256, 8),
+                                        (8, 1, 256, 9), (8, 1, 256, 16), (16, 1, 256, 40), (2, 2, 64, 1)])
+def test_short_chunks_at_the_borders_of_their_copies(hq, hkv, d, n):
+    """Chunks of exactly and just over a quarter, a half and the whole of a query tile, over ranges that end inside a
+    stage, a granule and a page."""
+    for L, window in ((n, 0), (n + 1, 0), (190, 0), (257, 20), (1027, 0), (2100, 1000)):
+        if L < n:
+            continue
+        c = Cache(hkv, d, [L, n + 3], seed=L + n).cuda()
+        _prefill_case(c, hq, [n, max(1, n - 1)], d ** -0.5, window, 7)
+
+
+def test_rescaled_rows_of_a_short_chunk():
+    """Scores that grow along the sequence, so that every stage moves the running maximum by far more than the lazy
+    threshold; and scores that fall, so that none does."""
+    for hq, hkv, d, n in ((4, 1, 128, 5), (4, 1, 128, 20), (8, 1, 64, 3), (8, 1, 256, 6), (8, 1, 256, 60)):
+        for up in (True, False):
+            c = Cache(hkv, d, [900], seed=3, spread=0.0)
+            for p in range(-(-900 // 16)):
+                c.ks[c.tables[0, p]] *= 0.5 * (p + 1) if up else 0.5 * (57 - p)
+            c.k = (c.k & 0x7F).astype(np.uint8)            # all keys positive: a score's size follows its page's scale
+            c.cuda()
+            starts = torch.tensor([0, n], dtype=torch.int32).cuda()
+            q = randn((n, hq, d), 5).abs()
+            out = f64(run_prefill(c, q.cuda(), starts, n, d ** -0.5))
+            check_rows(out, c, 0, f64(q), list(range(900 - n, 900)), d ** -0.5, 0, True, (d, n, up))

@@ -113,6 +113,15 @@ def test_prefill_block_validates(lib, kw, code):
     assert _prefill(lib, **kw) == code
 
 
+def test_stall_hook_validates(lib):
+    f = lib.fp8kv_debug_paged_prefill_block_stall
+    a = [FAKE, 64, FAKE, FAKE, FAKE, FAKE, 100, FAKE, 8, FAKE, FAKE, 64, 128, 2, 32, 8, 128, 16, 0.088, 0, FAKE, FAKE,
+         1 << 30, None]
+    assert f(*a, -1, 1000) == 1 and f(*a, 0, 0) == 1 and f(*a, 0, 500_000_001) == 1
+    a[16] = 96
+    assert f(*a, 0, 1000) == 2
+
+
 # ------------------------------------------------------------------ the binding
 
 def _bf(*shape):
