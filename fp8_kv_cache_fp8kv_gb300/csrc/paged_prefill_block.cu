@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
     __shared__ uint32_t tmem_base;
     __shared__ int abort_sh;
     __shared__ float4 psc[4][PAGES];
+    __shared__ float row_scale[RT];
     volatile int* abort_flag = &abort_sh;
     uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const uint32_t sb = smem_u32(sm);
@@ -125,20 +126,17 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
     // Lane p < GPAGES holds the block of page p of the stage to be copied next.
     const int ct = tid - kConvWarp0 * 32, grp = ct / GT, gt = ct % GT;   // (warps 4-11)
     auto granule_page = [&](int s) { return sp0 + s * PAGES + grp * GPAGES; };
+    // (The id as the table has it: looking at it here would wait for the read.)
     auto blocks_of = [&](int s) {
-        int id = 0;
         const int pg = granule_page(s) + lane;
-        if (lane < GPAGES && pg < sp1) {
-            id = __ldg(bt + pg);
-            if (id < 0 || id >= a.num_blocks) {
-                report(a.err, FP8KV_ERR_INVALID_ARG);
-                id = 0;
-            }
-        }
-        return id;
+        return lane < GPAGES && pg < sp1 ? __ldg(bt + pg) : 0;
     };
     auto load_granule = [&](int s, int ids) {
         const int np = sp1 - granule_page(s);     // pages left (<= 0 past the range)
+        if (ids < 0 || ids >= a.num_blocks) {     // block 0 is read instead
+            report(a.err, FP8KV_ERR_INVALID_ARG);
+            ids = 0;
+        }
         const uint32_t dst = sb + Og::STG + ((s % Og::STAGES) * Og::GROUPS + grp) * Og::GSLOT;
         constexpr int CPR = D / 16, CPP = kBS * CPR;   // 16-byte chunks per row, per page
 #pragma unroll
@@ -155,62 +153,72 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
         cp_async_commit();
     };
 
-    // ---- set-up: the rows build the Q tile (every copy its own); the
-    // converters start the first stages' copies
+    // ---- set-up: the converters start the first stages' copies, then all
+    // warps but the last build the Q tile
     const int part = (tid & 127) / RT;            // the row's copy (warps 0-3; the same for a warp)
     const int r = u.R0 + (tid & 127) % RT;
     const bool rv = warp < 4 && (tid & 127) % RT < a.rows && r < u.rows;
     int next_ids = 0;
-    float cs = 0.f;
-    int pq = 0, lq = 0, wpos0 = 0, wlo1 = 0;
-    if (warp < 4) {
-        constexpr int NC = D / 8;
-        const int tok = rv ? r >> lg : 0, hq = (hk << lg) + (rv ? r & ((1 << lg) - 1) : 0);
-        const uint4* qrow =
-            reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(u.q0 + tok) * a.num_q_heads + hq) * D);
-        float qmax = 0.f;
-#pragma unroll 8
-        for (int c = 0; c < NC; ++c) {
-            const uint4 qv = rv ? __ldg(qrow + c) : make_uint4(0, 0, 0, 0);
-            const uint32_t w4[4] = {qv.x, qv.y, qv.z, qv.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                qmax = fmaxf(qmax, fmaxf(fabsf(bf16_to_f32(w4[e] & 0xFFFF)), fabsf(bf16_to_f32(w4[e] >> 16))));
-        }
-        int shift = 0;
-        if (qmax > 0.f) {
-            const int e = static_cast<int>((__float_as_uint(qmax) >> 23) & 0xFF) - 127;
-            shift = max(-100, min(100, 14 - e));
-        }
-        // a negative score scale goes into Q: the row's scale cs is >= 0
-        const float up = (a.score_scale < 0.f ? -1.f : 1.f) * __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
-#pragma unroll 8
-        for (int c = 0; c < NC; ++c) {
-            const uint4 qv = rv ? __ldg(qrow + c) : make_uint4(0, 0, 0, 0);
-            const uint32_t w4[4] = {qv.x, qv.y, qv.z, qv.w};
-            uint32_t f[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                f[e] = pack_f16x2(bf16_to_f32(w4[e] & 0xFFFF) * up, bf16_to_f32(w4[e] >> 16) * up);
-            *reinterpret_cast<uint4*>(sm + Og::QT + (c >> 3) * 16384 + tid * 128 + (((c & 7) ^ (tid & 7)) << 4)) =
-                make_uint4(f[0], f[1], f[2], f[3]);
-        }
-        cs = fabsf(a.score_scale) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
-        pq = u.L - u.n + (rv ? r >> lg : 0);
-        lq = (a.window > 0 && pq + 1 > a.window) ? pq + 1 - a.window : 0;
-        // the warp's first position and its last valid row's window start: a
-        // stage of keys in [wlo1, wpos0] is attended in full by every row of the warp
-        const int wr0 = u.R0 + (warp * 32) % RT;
-        wpos0 = u.L - u.n + (wr0 >> lg);
-        const int wpos1 = u.L - u.n + (max(0, min(wr0 + 31, u.rows - 1)) >> lg);
-        wlo1 = (a.window > 0 && wpos1 + 1 > a.window) ? wpos1 + 1 - a.window : 0;
-    } else if (warp < kMmaWarp) {
+    if (warp >= kConvWarp0 && warp < kMmaWarp) {
         int ids[Og::STAGES];
 #pragma unroll
         for (int s = 0; s < Og::STAGES; ++s) ids[s] = blocks_of(s);
 #pragma unroll
         for (int s = 0; s < Og::STAGES - 1; ++s) load_granule(s, ids[s]);
         next_ids = ids[Og::STAGES - 1];
+    }
+    if (warp < kMmaWarp) {
+        // The Q tile, by warps 0-11: CL lanes share a row (a 16-byte chunk of 8
+        // values each, so the loads are coalesced and all of a thread's are in
+        // flight), find its largest magnitude by shuffles, and write the row as
+        // f16 -- once for every copy -- scaled by a power of two so that the
+        // copy of the bf16 values is exact.  A negative score scale goes into
+        // Q: the row's scale is >= 0.
+        constexpr int CL = D / 8, RPW = 32 / CL, NB0 = RT / (RPW * kMmaWarp) + 1;   // lanes per row, rows per warp and batch
+        const float sign = a.score_scale < 0.f ? -1.f : 1.f;
+        const int c = lane % CL;
+        uint4 qv[NB0];
+        auto row_of = [&](int i) { return (i * kMmaWarp + warp) * RPW + lane / CL; };   // row of the tile, batch i
+#pragma unroll
+        for (int i = 0; i < NB0; ++i) {
+            const int row = row_of(i), rr = u.R0 + row;
+            qv[i] = make_uint4(0, 0, 0, 0);
+            if (row < RT && rr < u.rows)
+                qv[i] = __ldg(reinterpret_cast<const uint4*>(
+                            a.q + (static_cast<int64_t>(u.q0 + (rr >> lg)) * a.num_q_heads + (hk << lg) +
+                                   (rr & ((1 << lg) - 1))) * D) + c);
+        }
+#pragma unroll
+        for (int i = 0; i < NB0; ++i) {
+            const int row = row_of(i);
+            const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+            float qmax = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                qmax = fmaxf(qmax, fmaxf(fabsf(bf16_to_f32(w4[e] & 0xFFFF)), fabsf(bf16_to_f32(w4[e] >> 16))));
+#pragma unroll
+            for (int off = CL / 2; off; off >>= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, off));
+            int shift = 0;
+            if (qmax > 0.f) {
+                const int e = static_cast<int>((__float_as_uint(qmax) >> 23) & 0xFF) - 127;
+                shift = max(-100, min(100, 14 - e));
+            }
+            const float up = sign * __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+            uint32_t f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                f[e] = pack_f16x2(bf16_to_f32(w4[e] & 0xFFFF) * up, bf16_to_f32(w4[e] >> 16) * up);
+            if (row < RT) {
+#pragma unroll
+                for (int o = 0; o < REP; ++o) {
+                    const int t = o * RT + row;
+                    *reinterpret_cast<uint4*>(sm + Og::QT + (c >> 3) * 16384 + t * 128 + (((c & 7) ^ (t & 7)) << 4)) =
+                        make_uint4(f[0], f[1], f[2], f[3]);
+                }
+                if (c == 0)
+                    row_scale[row] = fabsf(a.score_scale) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+            }
+        }
     }
     if (warp == 0) tc::alloc(&tmem_base, Og::COLS);
     tc::fence_proxy_async_smem();  // the Q tile is read by the tensor cores
@@ -223,6 +231,15 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
     float m = -INFINITY, l = 0.f;
     if (warp < 4) {
         // ---------------------------------------------------------- softmax
+        const float cs = row_scale[(tid & 127) % RT];
+        const int pq = u.L - u.n + (rv ? r >> lg : 0);
+        const int lq = (a.window > 0 && pq + 1 > a.window) ? pq + 1 - a.window : 0;
+        // the warp's first position and its last valid row's window start: a
+        // stage of keys in [wlo1, wpos0] is attended in full by every row of the warp
+        const int wr0 = u.R0 + (warp * 32) % RT;
+        const int wpos0 = u.L - u.n + (wr0 >> lg);
+        const int wpos1 = u.L - u.n + (max(0, min(wr0 + 31, u.rows - 1)) >> lg);
+        const int wlo1 = (a.window > 0 && wpos1 + 1 > a.window) ? wpos1 + 1 - a.window : 0;
         {
             float z[32];
 #pragma unroll
@@ -231,7 +248,7 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
             for (int c = 0; c < D / 32; ++c) tc::st32(trow + Og::OC + 32 * c, z);
             tc::wait_st();
         }
-        const bool warp_rows = u.R0 + (warp * 32) % RT < u.rows;   // a warp of no rows only keeps the handshake
+        const bool warp_rows = wr0 < u.rows;   // a warp of no rows only keeps the handshake
         PageScales<PAGES> feed(a, bt, hk, sp0, sp1, lane);
         for (int st = 0; st < nst; ++st) {
             const int buf = st & 1;

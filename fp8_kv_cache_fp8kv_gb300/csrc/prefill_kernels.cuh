@@ -724,30 +724,28 @@ struct PageScales {
     const Args& a;
     const int32_t* bt;   // the sequence's block-table row
     int hk, end, lane;   // kv head; first page past the range
-    int id;              // block of the page after next's stage, -1: none
+    int id;              // block of the page of the stage after next, as the table has it
     float k, v;          // next stage's scales
 
+    // The id as the table has it: looking at it here would wait for the read.
     __device__ __forceinline__ int block_of(int pg) const {
-        int b = -1;
-        if (lane < PAGES && pg + lane < end) {
-            b = __ldg(bt + pg + lane);
-            if (b < 0 || b >= a.num_blocks) b = 0;   // reported by the copies, which read block 0 too
-        }
-        return b;
+        return lane < PAGES && pg + lane < end ? __ldg(bt + pg + lane) : 0;
     }
-    __device__ __forceinline__ void fetch() {
+    // The scales of the pages at pg, whose ids are held; 1 past the range.  A
+    // bad id reads block 0's, as the copies do (they report it).
+    __device__ __forceinline__ void fetch(int pg) {
         k = v = 1.f;
-        if (id >= 0) {
-            const int64_t at = static_cast<int64_t>(id) * a.num_kv_heads + hk;
-            k = __ldg(a.k_page_scales + at);
-            v = __ldg(a.v_page_scales + at);
+        if (lane < PAGES && pg + lane < end) {
+            const int64_t b = id >= 0 && id < a.num_blocks ? id : 0;
+            k = __ldg(a.k_page_scales + b * a.num_kv_heads + hk);
+            v = __ldg(a.v_page_scales + b * a.num_kv_heads + hk);
         }
     }
     // Starts the reads of the stage at page pg and of the block ids after it.
     __device__ __forceinline__ PageScales(const Args& args, const int32_t* row, int head, int pg, int past, int ln)
         : a(args), bt(row), hk(head), end(past), lane(ln) {
         id = block_of(pg);
-        fetch();
+        fetch(pg);
         id = block_of(pg + PAGES);
     }
     // Publishes the scales of the stage at page pg; the reads move on.
@@ -755,7 +753,7 @@ struct PageScales {
         __syncwarp();            // the previous stage's entries have been read
         if (lane < PAGES) table[lane] = make_float4(k, log2f(v), 1.f / v, 0.f);
         __syncwarp();
-        fetch();
+        fetch(pg + PAGES);
         id = block_of(pg + 2 * PAGES);
     }
 };
