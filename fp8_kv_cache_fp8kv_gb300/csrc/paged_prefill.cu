@@ -79,11 +79,6 @@ inline int kernel_kind(int D, int tiles) {
 inline int block_kernel_kind(int D, int tiles) { return D == 256 || tiles == 1 ? kKindOne : kKindWs; }
 inline int tiles_per_cta(int kind) { return kind == kKindWs ? ws::kTiles : 1; }
 
-// Split overhead of the block-scaled one-tile kernel in pages (choose_splits):
-// its stages are so much shorter than the other kernels' that a CTA's fixed
-// cost weighs four times as many of them.
-constexpr int64_t kOneCtaPages = 32, kOneMergePages = 32;
-
 Plan make_plan(int batch, int max_q_len, int max_seq_len, int G, int Hkv, int D, int window, int sms, int per_sm,
                int kind) {
     Plan pl;
@@ -94,9 +89,7 @@ Plan make_plan(int batch, int max_q_len, int max_seq_len, int G, int Hkv, int D,
     const int64_t ctas = static_cast<int64_t>((pl.tiles + tpc - 1) / tpc) * Hkv * batch;
     int64_t pages = (static_cast<int64_t>(max_seq_len) + kBS - 1) / kBS;
     if (window > 0) pages = std::min<int64_t>(pages, (static_cast<int64_t>(window) + rows * tpc) / kBS + 2);
-    const int64_t slots_all = static_cast<int64_t>(sms) * per_sm;
-    pl.splits = kind == kKindOne ? choose_splits(ctas, pages, slots_all, kOneCtaPages, kOneMergePages)
-                                 : choose_splits(ctas, pages, slots_all);
+    pl.splits = choose_splits(ctas, pages, static_cast<int64_t>(sms) * per_sm);
     if (pl.splits > 1) {
         const size_t slots = static_cast<size_t>(units) * pl.splits * rows;
         pl.ml = kHeader;

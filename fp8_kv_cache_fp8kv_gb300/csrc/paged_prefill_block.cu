@@ -22,20 +22,26 @@ namespace prefill {
 // tiles: shared memory moves them in (fp8), out to the converting threads, in
 // again (f16, twice the bytes) and out to the MMAs, 224 KB per 32 KB of cache
 // at d = 128, 0.85 us of shared-memory bandwidth a stage.  Hence:
-//   * eight converter warps (4-11), in groups of 128 threads that each own a
-//     64-key granule (one group of 256 at d = 256): copies two stages ahead
-//     (one at d = 256), block ids one stage ahead of their copies, then K into
-//     the K tile (once the score MMAs of the stage before have read it) and V,
-//     transposed, into one of two V^T tiles;
+//   * two copy warps (14 for K, 15 for V) keep a ring of three stages (two at
+//     d = 256) filled with cp.async; a slot's barrier counts the copies as they
+//     land.  Block ids are read a stage before their copies;
+//   * eight converter warps (4-11): K into the K tile (once the score MMAs of the
+//     stage before have read it) and V, transposed, into one of two V^T tiles;
 //   * one thread of warp 12 issues the MMAs, the scores one stage ahead of the
 //     values: S has two buffers in tensor memory, so the softmax of a stage runs
-//     while the tensor cores compute the next stage's scores.  The MMAs of one
-//     thread run in issue order, which is what lets S(s + 1) overwrite the
-//     buffer that holds P(s - 1): O += P(s - 1) V was issued before it;
-//   * four softmax warps (0-3), thread = row = TMEM lane, P over S in TMEM, O
-//     summed by the tensor cores with the lazy rescale of the two-tile kernel.
-//     A rescale waits for the value MMAs of the stage before (their commit also
-//     frees the V^T tile); it is rare.
+//     while the tensor cores compute the next stage's scores.  (The MMAs of one
+//     thread run in issue order: S(s + 1) may overwrite S(s - 1), and the commit
+//     of S(s) tells that O += P(s - 2) V is done with its P buffer.);
+//   * warp 13 prepares the page scales, a stage ahead;
+//   * four softmax warps (0-3), thread = row = TMEM lane; P has two buffers of
+//     its own in tensor memory, and O is summed by the tensor cores, rescaled
+//     when the reference maximum of a row moves.  A stage is weighed under the
+//     reference the row already has, and only a page whose weights sum to more
+//     than 2^8 (or a row's first keys) makes the warp look for the maximum,
+//     rescale and weigh again: no maximum pass, one read of S.  A rescale waits
+//     for the value MMAs of the stage before (their commit also frees the V^T
+//     tile).  A load from tensor memory waits for value MMAs in flight, so a
+//     stage's scores are read before the P of the stage before is handed over;
 //   * REP: a chunk of at most 128 / REP rows fills the tile with REP copies of
 //     its rows, copy r taking the r-th part of every stage's keys (its P is zero
 //     elsewhere): each thread then runs 1 / REP of the softmax, which is what a
@@ -47,8 +53,10 @@ namespace one {
 constexpr int kConvWarp0 = 4;              // warps 4-11 convert
 constexpr int kConv = 8 * 32;
 constexpr int kMmaWarp = 12;
-constexpr int kThreads = 13 * 32;
-constexpr int kConvBar = 2;                // named barriers of the converter groups: 2, 3
+constexpr int kScaleWarp = 13;
+constexpr int kCopyWarp0 = 14;             // warp 14 copies K pages, warp 15 V pages
+constexpr int kThreads = 16 * 32;
+constexpr float kMaxSum = 256.f;           // a page's weights that sum to more move the row's reference
 }  // namespace one
 
 template <int D>
@@ -57,7 +65,6 @@ struct OneGeo {
     static constexpr int PAGES = KEYS / kBS;
     static constexpr int GROUPS = KEYS / tcg::kKeys;    // converter groups: 64-key granules per stage
     static constexpr int GT = one::kConv / GROUPS;      // threads of a group
-    static constexpr int GPAGES = tcg::kKeys / kBS;     // pages of a granule
     static constexpr int NB = D / 64;
     static constexpr int QTB = NB * 128 * 128;          // Q tile: 128 rows x d
     static constexpr int KAT = KEYS * 128;              // one 128-byte atom column of the K tile
@@ -68,17 +75,19 @@ struct OneGeo {
     static constexpr int STAGES = D == 256 ? 2 : 3;     // stages in the fp8 staging ring
     static constexpr int QT = 0, KT = QTB, VT = KT + KTB, STG = VT + 2 * VTB;
     static constexpr int SMEM = STG + STAGES * GROUPS * GSLOT;   // 224 KB at d = 256 and 128, 112 KB at 64
-    // TMEM: two S buffers (P written over the first half of each) at [0, KEYS)
-    // and [KEYS, 2 KEYS), the FP32 output accumulator at [256, 256 + d)
+    // TMEM columns: two S buffers from 0, the FP32 output accumulator (d) at OC,
+    // two P buffers (two keys a column) from PC
     static constexpr uint32_t OC = 256, COLS = 512;
-    static_assert(2 * KEYS <= 256 && OC + D <= COLS, "TMEM columns");
+    static constexpr uint32_t PC = D == 256 ? 2 * KEYS : OC + 128;
+    static_assert(2 * KEYS <= OC && OC + D <= COLS, "TMEM columns");
+    static_assert(D == 256 ? PC + KEYS <= OC : OC + D <= PC && PC + KEYS <= COLS, "TMEM columns");
 };
 
 template <int D, int REP>
 __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(const Args a) {
     using namespace one;
     using Og = OneGeo<D>;
-    constexpr int KEYS = Og::KEYS, PAGES = Og::PAGES, GT = Og::GT, GPAGES = Og::GPAGES;
+    constexpr int KEYS = Og::KEYS, PAGES = Og::PAGES, GT = Og::GT, STAGES = Og::STAGES;
     constexpr int RT = 128 / REP;                  // rows of the chunk in the tile
     constexpr int KP = KEYS / REP;                 // keys of a stage that one thread weighs
     constexpr int HK = KP > 64 ? 64 : KP;          // ... of which at once
@@ -87,10 +96,11 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
     static_assert(KP % 32 == 0, "whole TMEM loads");
     static_assert((REP - 1) * RT * (XS * 4 + 8) <= Og::STG - Og::KT, "the exchange fits over the operand tiles");
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t k_full, k_empty, v_full[2], v_empty[2], s_full[2], p_full[2], done_bar;
+    __shared__ uint64_t f_full[STAGES], f_empty[STAGES], c_full[2], k_full, k_empty, v_full[2], v_empty[2], s_full[2],
+        p_full[2], done_bar;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_sh;
-    __shared__ float4 psc[4][PAGES];
+    __shared__ float4 psc[2][PAGES];
     __shared__ float row_scale[RT];
     volatile int* abort_flag = &abort_sh;
     uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -104,6 +114,11 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
             mbar_init(&v_empty[j], 1);
             mbar_init(&s_full[j], 1);
             mbar_init(&p_full[j], 128);
+            mbar_init(&c_full[j], 1);      // the scale warp
+        }
+        for (int j = 0; j < STAGES; ++j) {
+            mbar_init(&f_full[j], 64);     // the copy warps' threads, as their copies land
+            mbar_init(&f_empty[j], kConv);
         }
         mbar_init(&done_bar, 1);
         abort_sh = 0;
@@ -122,50 +137,53 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
     const int nst = (sp1 - sp0 + PAGES - 1) / PAGES;
     const int32_t* bt = a.block_tables + static_cast<int64_t>(b) * a.max_blocks_per_seq;
 
-    // ---- converter group g's granule of a stage: pages [granule_page(s), ...).
-    // Lane p < GPAGES holds the block of page p of the stage to be copied next.
-    const int ct = tid - kConvWarp0 * 32, grp = ct / GT, gt = ct % GT;   // (warps 4-11)
-    auto granule_page = [&](int s) { return sp0 + s * PAGES + grp * GPAGES; };
-    // (The id as the table has it: looking at it here would wait for the read.)
+    // ---- set-up: the copy warps start the first stages' copies, the softmax
+    // and converter warps build the Q tile
+    const int part = (tid & 127) / RT;            // the row's copy (warps 0-3; the same for a warp)
+    const int r = u.R0 + (tid & 127) % RT;
+    const bool rv = warp < 4 && (tid & 127) % RT < a.rows && r < u.rows;
+    // Stage s's block ids, lane p holding page p's as the table has it (looking
+    // at it here would wait for the read).
     auto blocks_of = [&](int s) {
-        const int pg = granule_page(s) + lane;
-        return lane < GPAGES && pg < sp1 ? __ldg(bt + pg) : 0;
+        const int pg = sp0 + s * PAGES + lane;
+        return lane < PAGES && pg < sp1 ? __ldg(bt + pg) : 0;
     };
-    auto load_granule = [&](int s, int ids) {
-        const int np = sp1 - granule_page(s);     // pages left (<= 0 past the range)
+    // A copy warp's half of stage s (K rows or V rows) into its ring slot; the
+    // slot's barrier counts the copies as they land.
+    const bool copy_v = warp == kCopyWarp0 + 1;
+    auto copy_stage = [&](int s, int ids) {
+        const int np = min(PAGES, sp1 - sp0 - s * PAGES);
         if (ids < 0 || ids >= a.num_blocks) {     // block 0 is read instead
             report(a.err, FP8KV_ERR_INVALID_ARG);
             ids = 0;
         }
-        const uint32_t dst = sb + Og::STG + ((s % Og::STAGES) * Og::GROUPS + grp) * Og::GSLOT;
-        constexpr int CPR = D / 16, CPP = kBS * CPR;   // 16-byte chunks per row, per page
+        const uint8_t* cache = copy_v ? a.v_cache : a.k_cache;
+        const uint32_t slot = sb + Og::STG + (s % STAGES) * (Og::GROUPS * Og::GSLOT) + (copy_v ? tcg::kKeys * D : 0);
+        constexpr int CPR = D / 16;               // 16-byte chunks per row; a page's rows are contiguous
 #pragma unroll
-        for (int it = 0; it < GPAGES * CPP / GT; ++it) {
-            const int i = gt + it * GT, p = i / CPP, ci = i % CPP;   // p is the same for a warp
+        for (int p = 0; p < PAGES; ++p) {
             const int id = __shfl_sync(0xffffffffu, ids, p);
             if (p < np) {
-                const int r = ci / CPR, c = ci % CPR, k = p * kBS + r;
-                const int64_t src = (static_cast<int64_t>(id) * a.num_kv_heads + hk) * (kBS * D) + r * D + c * 16;
-                cp_async16(dst + stg_k<D>(k, c), a.k_cache + src);
-                cp_async16(dst + tcg::kKeys * D + stg_v<D>(k, c), a.v_cache + src);
+                const uint8_t* src = cache + (static_cast<int64_t>(id) * a.num_kv_heads + hk) * (kBS * D) + lane * 16;
+                const uint32_t dst = slot + (p / 4) * Og::GSLOT;
+#pragma unroll
+                for (int i = 0; i < kBS * CPR / 32; ++i) {
+                    const int ci = lane + 32 * i, k = (p % 4) * kBS + ci / CPR, c = ci % CPR;
+                    cp_async16(dst + (copy_v ? stg_v<D>(k, c) : stg_k<D>(k, c)), src + 512 * i);
+                }
             }
         }
-        cp_async_commit();
+        cp_async_mbar_arrive(&f_full[s % STAGES]);
     };
-
-    // ---- set-up: the converters start the first stages' copies, then all
-    // warps but the last build the Q tile
-    const int part = (tid & 127) / RT;            // the row's copy (warps 0-3; the same for a warp)
-    const int r = u.R0 + (tid & 127) % RT;
-    const bool rv = warp < 4 && (tid & 127) % RT < a.rows && r < u.rows;
     int next_ids = 0;
-    if (warp >= kConvWarp0 && warp < kMmaWarp) {
-        int ids[Og::STAGES];
+    if (warp >= kCopyWarp0) {
+        int ids[STAGES + 1];
 #pragma unroll
-        for (int s = 0; s < Og::STAGES; ++s) ids[s] = blocks_of(s);
+        for (int s = 0; s <= STAGES; ++s) ids[s] = blocks_of(s);
 #pragma unroll
-        for (int s = 0; s < Og::STAGES - 1; ++s) load_granule(s, ids[s]);
-        next_ids = ids[Og::STAGES - 1];
+        for (int s = 0; s < STAGES; ++s)
+            if (s < nst) copy_stage(s, ids[s]);
+        next_ids = ids[STAGES];
     }
     if (warp < kMmaWarp) {
         // The Q tile, by warps 0-11: CL lanes share a row (a 16-byte chunk of 8
@@ -241,153 +259,175 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
         const int wpos1 = u.L - u.n + (max(0, min(wr0 + 31, u.rows - 1)) >> lg);
         const int wlo1 = (a.window > 0 && wpos1 + 1 > a.window) ? wpos1 + 1 - a.window : 0;
         {
+            // O starts at zero; so does P, of which each copy then writes its own part only
             float z[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) z[j] = 0.f;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) tc::st32(trow + Og::OC + 32 * c, z);
+#pragma unroll
+            for (int c = 0; c < KEYS / 32; ++c) tc::st32(trow + Og::PC + 32 * c, z);
             tc::wait_st();
         }
         const bool warp_rows = wr0 < u.rows;   // a warp of no rows only keeps the handshake
-        PageScales<PAGES> feed(a, bt, hk, sp0, sp1, lane);
-        for (int st = 0; st < nst; ++st) {
-            const int buf = st & 1;
-            bool ok = wait_or_abort(&s_full[buf], (st >> 1) & 1, a.wait_ns, abort_flag);
-            if (!__all_sync(0xffffffffu, ok)) break;   // warp-uniform: the TMEM loads below are collective
-            if (warp_rows) {
+        // (the waits' results are made warp-uniform: the TMEM loads are collective)
+        auto wait_s = [&](int s) {
+            return __all_sync(0xffffffffu, wait_or_abort(&s_full[s & 1], (s >> 1) & 1, a.wait_ns, abort_flag));
+        };
+        // this copy's scores of stage s, HK at a time
+        float sv[HK];
+        auto load = [&](int s, int h) {
+            const uint32_t scol = trow + (s & 1) * KEYS + part * KP + HK * h;
+#pragma unroll
+            for (int c = 0; c < HK / 32; ++c)
+                tc::ld32(scol + 32 * c, *reinterpret_cast<float(*)[32]>(sv + 32 * c));
+#pragma unroll
+            for (int c = 0; c < HK / 32; ++c) tc::wait_ld(*reinterpret_cast<float(*)[32]>(sv + 32 * c));
+        };
+        bool ok = true;
+        if (NH == 1 && nst > 0) {
+            ok = wait_s(0);
+            if (ok && warp_rows) {
                 tc::fence_after_sync();
+                load(0, 0);
+            }
+        }
+        for (int st = 0; st < nst && ok; ++st) {
+            const int buf = st & 1;
+            if (NH > 1 && !wait_s(st)) break;
+            if (!__all_sync(0xffffffffu, wait_or_abort(&c_full[buf], (st >> 1) & 1, a.wait_ns, abort_flag))) break;
+            if (warp_rows) {
+                if (NH > 1) tc::fence_after_sync();
                 const int pgs = sp0 + st * PAGES;
                 const int nk = min(PAGES, sp1 - pgs) * kBS;         // the stage's keys
                 const int t0 = pgs * kBS;
                 const bool interior = nk == KEYS && t0 + KEYS - 1 <= wpos0 && t0 >= wlo1;
-                const uint32_t scol = trow + buf * KEYS + part * KP;           // this copy's scores
-                const uint32_t pcol = trow + buf * KEYS + part * (KP / 2);     // and its P, two keys a column
-                feed.publish(psc[warp], pgs);
-                const float4* scale = psc[warp] + part * (KP / kBS);
-                auto load = [&](int h, float (&sv)[HK]) {
-#pragma unroll
-                    for (int c = 0; c < HK / 32; ++c)
-                        tc::ld32(scol + HK * h + 32 * c, *reinterpret_cast<float(*)[32]>(sv + 32 * c));
-#pragma unroll
-                    for (int c = 0; c < HK / 32; ++c) tc::wait_ld(*reinterpret_cast<float(*)[32]>(sv + 32 * c));
-                };
+                const uint32_t pcol = trow + Og::PC + buf * (KEYS / 2) + part * (KP / 2);  // this copy's P, two keys a column
+                const float4* scale = psc[buf] + part * (KP / kBS);
                 auto key_ok = [&](int jj) {   // jj: key of the stage
                     const int key = t0 + jj;
                     return jj < nk && rv && key >= lq && key <= pq;
                 };
-                float mx = -INFINITY;
-                auto maxima = [&](int h, const float (&sv)[HK]) {
-                    // page by page: the largest raw score, scaled (cs and the
-                    // K scale are >= 0), plus the V scale's logarithm
-#pragma unroll
-                    for (int pp = 0; pp < HK / kBS; ++pp) {
-                        float mp[2] = {-INFINITY, -INFINITY};
-                        if (interior) {
-#pragma unroll
-                            for (int i = 0; i < kBS; ++i) mp[i & 1] = fmaxf(mp[i & 1], sv[kBS * pp + i]);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < kBS; ++i)
-                                mp[i & 1] = fmaxf(mp[i & 1], key_ok(part * KP + HK * h + kBS * pp + i) ? sv[kBS * pp + i]
-                                                                                                      : -INFINITY);
-                        }
-                        const float big = fmaxf(mp[0], mp[1]);
-                        const float4 w = scale[HK / kBS * h + pp];
-                        if (big != -INFINITY) mx = fmaxf(mx, fmaf(big, cs * w.x, w.y));
-                    }
-                };
-                float sv[HK];
-                if constexpr (NH == 1) {
-                    load(0, sv);
-                    maxima(0, sv);
-                } else {   // the scores are read twice, 64 at a time
+                // The part's weights under the reference maximum m, into P;
+                // their sum over the V scales, and the largest sum of a page's.
+                float ls, top = 0.f;
+                auto weigh = [&]() {
+                    ls = 0.f;
+                    top = 0.f;
+                    const float nmuse = m == -INFINITY ? 0.f : -m;
 #pragma unroll 1
                     for (int h = 0; h < NH; ++h) {
-                        load(h, sv);
-                        maxima(h, sv);
+                        if constexpr (NH > 1) load(st, h);
+#pragma unroll
+                        for (int p2 = 0; p2 < HK / 32; ++p2) {   // two pages: 16 columns of P
+                            float pw[16];
+#pragma unroll
+                            for (int pp = 0; pp < 2; ++pp) {
+                                const int page = 2 * p2 + pp;
+                                const float4 w = scale[HK / kBS * h + page];
+                                const float c = cs * w.x, n = w.y + nmuse;
+                                float ps[2] = {0.f, 0.f};
+                                if (interior) {
+#pragma unroll
+                                    for (int i = 0; i < kBS / 2; ++i) {   // key pairs in packed FP32 pairs
+                                        const int j = kBS * page + 2 * i;
+                                        float x0, x1;
+                                        fma_f32x2(x0, x1, sv[j], sv[j + 1], c, c, n, n);
+                                        const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                                        add_f32x2(ps[0], ps[1], p0, p1);
+                                        pw[8 * pp + i] = __uint_as_float(pack_f16x2(p0, p1));
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < kBS / 2; ++i) {   // masked keys weigh 0 (also when cs = 0)
+                                        const int j = kBS * page + 2 * i, jj = part * KP + HK * h + j;
+                                        const float p0 = key_ok(jj) ? fast_exp2(fmaf(sv[j], c, n)) : 0.f;
+                                        const float p1 = key_ok(jj + 1) ? fast_exp2(fmaf(sv[j + 1], c, n)) : 0.f;
+                                        ps[0] += p0;
+                                        ps[1] += p1;
+                                        pw[8 * pp + i] = __uint_as_float(pack_f16x2(p0, p1));
+                                    }
+                                }
+                                const float sum = ps[0] + ps[1];
+                                ls = fmaf(sum, w.z, ls);
+                                top = fmaxf(top, sum);
+                            }
+                            tc::st16(pcol + HK / 2 * h + 16 * p2, pw);
+                        }
                     }
+                };
+                // First under the reference the row has, which mostly still
+                // holds: the scores are read once and no maximum is looked for.
+                // A row's first keys, or a page whose weights sum to more than
+                // 2^8 (no weight of a smaller sum is above it, so all are f16),
+                // send the warp the long way.
+                const int k0 = t0 + part * KP, k1 = min(t0 + nk, k0 + KP) - 1;
+                bool look = __any_sync(0xffffffffu, m == -INFINITY && rv && pq >= k0 && lq <= k1 && k0 <= k1);
+#pragma unroll 1
+                while (true) {
+                    if (look) {
+                        // page by page (from tensor memory again, in a loop:
+                        // this path is rare and should be small): the largest
+                        // raw score, scaled (cs and the K scale are >= 0),
+                        // plus the V scale's logarithm
+                        float mx = -INFINITY;
+#pragma unroll 1
+                        for (int pg = 0; pg < KP / kBS; ++pg) {
+                            float x[16], big = -INFINITY;
+                            tc::ld16(trow + buf * KEYS + part * KP + kBS * pg, x);
+                            tc::wait_ld(x);
+#pragma unroll
+                            for (int i = 0; i < kBS; ++i) big = fmaxf(big, key_ok(part * KP + kBS * pg + i) ? x[i] : -INFINITY);
+                            const float4 w = scale[pg];
+                            mx = fmaxf(mx, big == -INFINITY ? -INFINITY : fmaf(big, cs * w.x, w.y));
+                        }
+                        // such a row's reference moves to its maximum; a row that
+                        // had none (m = -inf) holds O = 0 and l = 0
+                        const float mn = fmaxf(m, mx);
+                        const bool upd = mn > m && (m == -INFINITY || top > kMaxSum);
+                        const bool held = upd && m != -INFINITY;
+                        float alpha = 1.f;
+                        if (upd) {
+                            alpha = fast_exp2(m - mn);
+                            l *= alpha;
+                            m = mn;
+                        }
+                        if (__any_sync(0xffffffffu, held)) {
+                            // O = O * alpha for the warp's rows, once the value MMAs of stage st - 1 are in
+                            ok = __all_sync(0xffffffffu, wait_or_abort(&v_empty[buf ^ 1], ((st - 1) >> 1) & 1, a.wait_ns,
+                                                                       abort_flag));
+                            if (!ok) break;
+                            tc::fence_after_sync();
+#pragma unroll 1
+                            for (int c = 0; c < D / 16; ++c) {   // (16 at a time: the scores are in registers)
+                                float x[16];
+                                tc::ld16(trow + Og::OC + 16 * c, x);
+                                tc::wait_ld(x);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) x[j] *= alpha;
+                                tc::st16(trow + Og::OC + 16 * c, x);
+                            }
+                        }
+                    }
+                    weigh();
+                    if (look) break;
+                    look = __any_sync(0xffffffffu, top > kMaxSum);
+                    if (!look) break;
                 }
-                // the reference maximum moves only by more than 8 (log2 units);
-                // a row that had none (m = -inf) holds O = 0 and l = 0
-                const float mn = fmaxf(m, mx);
-                const bool upd = mn > m + ws::kRescaleLog2;
-                const bool held = upd && m != -INFINITY;
-                float alpha = 1.f;
-                if (upd) {
-                    alpha = fast_exp2(m - mn);
-                    l *= alpha;
-                    m = mn;
-                }
-                if (__any_sync(0xffffffffu, held)) {
-                    // O = O * alpha for the warp's rows, once the value MMAs of stage st - 1 are in
-                    ok = wait_or_abort(&v_empty[buf ^ 1], ((st - 1) >> 1) & 1, a.wait_ns, abort_flag);
-                    if (!__all_sync(0xffffffffu, ok)) break;
+                if (!ok) break;
+                l += ls;
+            }
+            if (NH == 1 && st + 1 < nst) {
+                // the next stage's scores move to registers before P is handed
+                // over: a load would wait for the value MMAs, which then run
+                ok = wait_s(st + 1);
+                if (!ok) break;
+                if (warp_rows) {
                     tc::fence_after_sync();
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        float x[32];
-                        tc::ld32(trow + Og::OC + 32 * c, x);
-                        tc::wait_ld(x);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] *= alpha;
-                        tc::st32(trow + Og::OC + 32 * c, x);
-                    }
+                    load(st + 1, 0);
                 }
-                const float nmuse = m == -INFINITY ? 0.f : -m;
-                auto weights = [&](int h) {
-                    float pw[HK / 2];
-#pragma unroll
-                    for (int pp = 0; pp < HK / kBS; ++pp) {
-                        const float4 w = scale[HK / kBS * h + pp];
-                        const float c = cs * w.x, n = w.y + nmuse;
-                        float ps[2] = {0.f, 0.f};
-                        if (interior) {
-#pragma unroll
-                            for (int i = 0; i < kBS / 2; ++i) {   // key pairs in packed FP32 pairs
-                                const int j = kBS / 2 * pp + i;
-                                float x0, x1;
-                                fma_f32x2(x0, x1, sv[2 * j], sv[2 * j + 1], c, c, n, n);
-                                const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                                add_f32x2(ps[0], ps[1], p0, p1);
-                                pw[j] = __uint_as_float(pack_f16x2(p0, p1));
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < kBS / 2; ++i) {   // masked keys weigh 0 (also when cs = 0)
-                                const int j = kBS / 2 * pp + i, jj = part * KP + HK * h + 2 * j;
-                                const float p0 = key_ok(jj) ? fast_exp2(fmaf(sv[2 * j], c, n)) : 0.f;
-                                const float p1 = key_ok(jj + 1) ? fast_exp2(fmaf(sv[2 * j + 1], c, n)) : 0.f;
-                                ps[0] += p0;
-                                ps[1] += p1;
-                                pw[j] = __uint_as_float(pack_f16x2(p0, p1));
-                            }
-                        }
-                        l = fmaf(ps[0] + ps[1], w.z, l);
-                    }
-                    if constexpr (HK == 64) tc::st32(pcol + 32 * h, *reinterpret_cast<float(*)[32]>(pw));
-                    else tc::st16(pcol + 16 * h, *reinterpret_cast<float(*)[16]>(pw));
-                };
-                if constexpr (NH == 1) {
-                    weights(0);
-                } else {
-#pragma unroll 1
-                    for (int h = 0; h < NH; ++h) {
-                        // P of half h goes to columns whose S (of half h / 2 and below) has been read
-                        load(h, sv);
-                        weights(h);
-                    }
-                }
-                if constexpr (REP > 1) {   // the other copies' keys weigh 0 (their scores in this lane are not needed)
-                    float z[KP / 2];
-#pragma unroll
-                    for (int j = 0; j < KP / 2; ++j) z[j] = 0.f;
-#pragma unroll
-                    for (int o = 1; o < REP; ++o) {
-                        const uint32_t col = trow + buf * KEYS + ((part + o) % REP) * (KP / 2);
-                        if constexpr (KP == 64) tc::st32(col, *reinterpret_cast<float(*)[32]>(z));
-                        else tc::st16(col, *reinterpret_cast<float(*)[16]>(z));
-                    }
-                }
+            }
+            if (warp_rows) {
                 tc::wait_st();
                 tc::fence_before_sync();
             }
@@ -395,31 +435,51 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
         }
     } else if (warp < kMmaWarp) {
         // ---------------------------------------------------------- converters
+        const int ct = tid - kConvWarp0 * 32, grp = ct / GT, gt = ct % GT;
         for (int st = 0; st < nst; ++st) {
-            load_granule(st + Og::STAGES - 1, next_ids);   // its slot was read in iteration st - 1
-            next_ids = blocks_of(st + Og::STAGES);
-            cp_async_wait<Og::STAGES - 1>();               // this thread's copies of stage st have landed
-            const uint8_t* stg = sm + Og::STG + ((st % Og::STAGES) * Og::GROUPS + grp) * Og::GSLOT;
-            const int pg = granule_page(st);
-            // the K tile is free once the score MMAs of stage st - 1 have completed
-            bool ok = st == 0 || wait_or_abort(&k_empty, (st - 1) & 1, a.wait_ns, abort_flag);
-            if (named_bar_or(kConvBar + grp, GT, !ok)) break;   // the group's copies landed (or all of it gives up)
+            const int slot = st % STAGES;
+            const uint8_t* stg = sm + Og::STG + (slot * Og::GROUPS + grp) * Og::GSLOT;
+            const int pg = sp0 + st * PAGES + grp * (tcg::kKeys / kBS);
+            // stage st's pages have landed; the K tile is free once the score
+            // MMAs of stage st - 1 have completed
+            if (!wait_or_abort(&f_full[slot], (st / STAGES) & 1, a.wait_ns, abort_flag)) break;
+            if (st > 0 && !wait_or_abort(&k_empty, (st - 1) & 1, a.wait_ns, abort_flag)) break;
             if (pg < sp1)                                       // an empty granule's keys are masked
                 convert_stage_k<D, Og::KAT, GT>(stg, sm + Og::KT + grp * (tcg::kKeys * 128), gt);
             tc::fence_proxy_async_smem();                       // the tile is read by the tensor cores
             mbar_arrive(&k_full);
             // V^T tile st & 1 is free once the value MMAs of stage st - 2 have completed
             const int j = st & 1;
-            ok = st < 2 || wait_or_abort(&v_empty[j], ((st >> 1) + 1) & 1, a.wait_ns, abort_flag);
-            if (named_bar_or(kConvBar + grp, GT, !ok)) break;
-            convert_stage_v<D, GT>(stg, sm + Og::VT + j * Og::VTB + grp * Og::VAT, gt, pg * kBS, min(GPAGES, sp1 - pg),
-                                   u.kmin, u.kmax);             // zeros past the range
+            if (st >= 2 && !wait_or_abort(&v_empty[j], ((st >> 1) + 1) & 1, a.wait_ns, abort_flag)) break;
+            convert_stage_v<D, GT>(stg, sm + Og::VT + j * Og::VTB + grp * Og::VAT, gt, pg * kBS,
+                                   min(tcg::kKeys / kBS, sp1 - pg), u.kmin, u.kmax);   // zeros past the range
             tc::fence_proxy_async_smem();
             mbar_arrive(&v_full[j]);
-            named_bar_sync(kConvBar + grp, GT);                 // the granule is read before it is refilled
+            mbar_arrive(&f_empty[slot]);
         }
-        cp_async_wait<0>();
-    } else if (lane == 0) {
+    } else if (warp >= kCopyWarp0) {
+        // ---------------------------------------------------------- copies
+        for (int st = STAGES; st < nst; ++st) {
+            if (!__all_sync(0xffffffffu, wait_or_abort(&f_empty[st % STAGES], (st / STAGES + 1) & 1, a.wait_ns, abort_flag)))
+                break;
+            copy_stage(st, next_ids);
+            next_ids = blocks_of(st + 1);
+        }
+        cp_async_wait_all();               // no copy lands after the CTA is gone
+    } else if (warp == kScaleWarp) {
+        // ---------------------------------------------------------- page scales
+        PageScales<PAGES> feed(a, bt, hk, sp0, sp1, lane);
+        for (int st = 0; st < nst; ++st) {
+            // the table was last read for stage st - 2, before its P was handed over
+            if (st >= 2 &&
+                !__all_sync(0xffffffffu, wait_or_abort(&p_full[st & 1], ((st >> 1) + 1) & 1, a.wait_ns, abort_flag)))
+                break;
+            feed.write(psc[st & 1]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c_full[st & 1]);
+            feed.advance(sp0 + st * PAGES);
+        }
+    } else if (lane == 0) {   // (of warp 12)
         // ---------------------------------------------------------- MMA issuer
         constexpr uint32_t id_s = tc::idesc_f16_f32(128, KEYS);
         constexpr uint32_t id_o = tc::idesc_f16_f32(128, D);
@@ -447,10 +507,10 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
                 !wait_or_abort(&v_full[st & 1], (st >> 1) & 1, a.wait_ns, abort_flag))
                 break;
             tc::fence_after_sync();
-            // O += P V: P (128 rows x KEYS) from the first half of the stage's S columns
+            // O += P V: P (128 rows x KEYS) from tensor memory
 #pragma unroll
             for (int ks = 0; ks < KEYS / 16; ++ks)
-                tc::mma_f16_ts(tm + Og::OC, tm + (st & 1) * KEYS + ks * 8,
+                tc::mma_f16_ts(tm + Og::OC, tm + Og::PC + (st & 1) * (KEYS / 2) + ks * 8,
                                tc::desc_k_sw128(sb + Og::VT + (st & 1) * Og::VTB + (ks >> 2) * Og::VAT + (ks & 3) * 32),
                                id_o, 1);
             tc::commit(&v_empty[st & 1]);        // the V^T tile is free, and O complete, when the value MMAs complete

@@ -748,13 +748,21 @@ struct PageScales {
         fetch(pg);
         id = block_of(pg + PAGES);
     }
-    // Publishes the scales of the stage at page pg; the reads move on.
-    __device__ __forceinline__ void publish(float4* table, int pg) {
-        __syncwarp();            // the previous stage's entries have been read
+    // The stage's entries into the table.
+    __device__ __forceinline__ void write(float4* table) const {
         if (lane < PAGES) table[lane] = make_float4(k, log2f(v), 1.f / v, 0.f);
-        __syncwarp();
+    }
+    // The reads move on from the stage at page pg.
+    __device__ __forceinline__ void advance(int pg) {
         fetch(pg + PAGES);
         id = block_of(pg + 2 * PAGES);
+    }
+    // Both, for a table of the warp's own.
+    __device__ __forceinline__ void publish(float4* table, int pg) {
+        __syncwarp();            // the previous stage's entries have been read
+        write(table);
+        __syncwarp();
+        advance(pg);
     }
 };
 

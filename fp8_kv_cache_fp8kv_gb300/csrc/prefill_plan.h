@@ -24,12 +24,11 @@ constexpr int64_t kMergePages = 4;
 
 // units: CTAs without splitting; pages: the most key pages a unit attends;
 // slots: CTAs resident at once on the device (SMs x CTAs per SM).
-inline int choose_splits(int64_t units, int64_t pages, int64_t slots, int64_t cta_pages = kSplitCtaPages,
-                         int64_t merge_pages = kMergePages) {
+inline int choose_splits(int64_t units, int64_t pages, int64_t slots) {
     if (units <= 0 || slots <= 0 || units >= slots) return 1;
     auto cost = [&](int64_t sp) {
         const int64_t waves = (units * sp + slots - 1) / slots;
-        return waves * ((pages + sp - 1) / sp + cta_pages) + (sp > 1 ? merge_pages : 0);
+        return waves * ((pages + sp - 1) / sp + kSplitCtaPages) + (sp > 1 ? kMergePages : 0);
     };
     int best = 1;
     int64_t best_cost = cost(1);

@@ -107,6 +107,15 @@ __device__ __forceinline__ void cp_async_4(uint32_t smem_dst, const void* src) {
 // Closes the calling thread's current group of cp.async copies.
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
+// Arrives (once) on `bar` when all cp.async copies of the calling thread so far
+// have landed; the arrival is one of those the barrier was initialised for.
+__device__ __forceinline__ void cp_async_mbar_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Waits until all of the calling thread's copies have landed.
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Waits until at most N of the calling thread's most recent copy groups are
 // still in flight.  Copies always complete: this wait ends by itself.
 template <int N>
