@@ -14,6 +14,117 @@ namespace fp8kv {
 namespace prefill {
 
 // ---------------------------------------------------------------------------
+// What the two kernels share.
+
+// A unit's query rows [R0, R0 + ROWS) as f16 tiles of 128 rows x d at `qt`,
+// by the NW warps wi = 0 .. NW - 1: CL lanes share a row (a 16-byte chunk of 8
+// values each, so the loads are coalesced and all of a thread's are in
+// flight), find its largest magnitude by shuffles, and write the row -- REP
+// times, ROWS apart -- scaled by a power of two so that the copy of the bf16
+// values is exact.  row_scale is what takes a raw score back into log2 units.
+// A negative score scale goes into Q, so row_scale is positive; at least
+// 1e-30, so that a masked score of -inf stays one under a score scale of zero
+// (no raw score reaches 2^40: its product with 1e-30 is zero to every sum).
+template <int D, int ROWS, int REP, int NW>
+__device__ __forceinline__ void build_q_tiles(const Args& a, const Unit& u, int hk, int R0, uint8_t* qt,
+                                              float* row_scale, int wi, int lane) {
+    constexpr int CL = D / 8, RPW = 32 / CL;                     // lanes per row, rows per warp and batch
+    constexpr int NB = (ROWS + RPW * NW - 1) / (RPW * NW);       // batches
+    constexpr int QTB = D / 64 * 16384;                          // bytes of a tile
+    const int lg = a.log2_group, c = lane % CL;
+    const float sign = a.score_scale < 0.f ? -1.f : 1.f;
+    uint4 qv[NB];
+    auto row_of = [&](int i) { return (i * NW + wi) * RPW + lane / CL; };
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        const int row = row_of(i), rr = R0 + row;
+        qv[i] = make_uint4(0, 0, 0, 0);
+        if (row < ROWS && rr < u.rows)
+            qv[i] = __ldg(reinterpret_cast<const uint4*>(
+                        a.q + (static_cast<int64_t>(u.q0 + (rr >> lg)) * a.num_q_heads + (hk << lg) +
+                               (rr & ((1 << lg) - 1))) * D) + c);
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        const int row = row_of(i);
+        const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+        float qmax = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            qmax = fmaxf(qmax, fmaxf(fabsf(bf16_to_f32(w4[e] & 0xFFFF)), fabsf(bf16_to_f32(w4[e] >> 16))));
+#pragma unroll
+        for (int off = CL / 2; off; off >>= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, off));
+        int shift = 0;
+        if (qmax > 0.f) {
+            const int e = static_cast<int>((__float_as_uint(qmax) >> 23) & 0xFF) - 127;
+            shift = max(-100, min(100, 14 - e));
+        }
+        const float up = sign * __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+        uint32_t f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            f[e] = pack_f16x2(bf16_to_f32(w4[e] & 0xFFFF) * up, bf16_to_f32(w4[e] >> 16) * up);
+        if (row < ROWS) {
+#pragma unroll
+            for (int o = 0; o < REP; ++o) {
+                const int t = o * ROWS + row;
+                *reinterpret_cast<uint4*>(qt + (t >> 7) * QTB + (c >> 3) * 16384 + (t & 127) * 128 +
+                                          (((c & 7) ^ (t & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
+            }
+            if (c == 0)
+                row_scale[row] =
+                    fmaxf(fabsf(a.score_scale) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23), 1e-30f);
+        }
+    }
+}
+
+// The weights of HK keys of one row under the reference maximum m: w = 2^(s cs
+// ks + log2 vs - m), as f16 pairs into the TMEM columns from pcol, their sum
+// over the V scales added to ls, and the largest sum of a page's in top.
+// Masked scores are -inf.  Key pairs go through packed FP32 pairs.
+template <int HK>
+__device__ __forceinline__ void weigh_keys(const float (&sv)[HK], const float4* scale, float cs, float m, uint32_t pcol,
+                                           float& ls, float& top) {
+    const float nmuse = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+    for (int p2 = 0; p2 < HK / 32; ++p2) {   // two pages: 16 columns of P
+        float pw[16];
+#pragma unroll
+        for (int pp = 0; pp < 2; ++pp) {
+            const float4 w = scale[2 * p2 + pp];
+            const float c = cs * w.x, n = w.y + nmuse;
+            float ps[2] = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < kBS / 2; ++i) {
+                const int j = kBS * (2 * p2 + pp) + 2 * i;
+                float x0, x1;
+                fma_f32x2(x0, x1, sv[j], sv[j + 1], c, c, n, n);
+                const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                add_f32x2(ps[0], ps[1], p0, p1);
+                pw[8 * pp + i] = __uint_as_float(pack_f16x2(p0, p1));
+            }
+            const float sum = ps[0] + ps[1];
+            ls = fmaf(sum, w.z, ls);
+            top = fmaxf(top, sum);
+        }
+        tc::st16(pcol + 16 * p2, pw);
+    }
+}
+
+// Scores of HK keys from position `key0` on that a row may not attend become
+// -inf: it attends [lq, pq], of which the stage has keys below `end`.
+template <int HK>
+__device__ __forceinline__ void mask_keys(float (&sv)[HK], int key0, int lq, int pq, int end) {
+    const int lo = lq - key0, hi = min(pq, end - 1) - key0;
+#pragma unroll
+    for (int j = 0; j < HK; ++j) sv[j] = j >= lo && j <= hi ? sv[j] : -INFINITY;
+}
+
+// A page whose weights under a row's reference sum to more than this moves the
+// reference.  No weight of a smaller sum is above it, so all are f16.
+constexpr float kMaxSum = 256.f;
+
+// ---------------------------------------------------------------------------
 // The one-tile kernel: 128 query rows of one (sequence, kv head) per CTA and
 // one key range, in stages of 128 keys (64 at d = 256).
 //
@@ -56,7 +167,6 @@ constexpr int kMmaWarp = 12;
 constexpr int kScaleWarp = 13;
 constexpr int kCopyWarp0 = 14;             // warp 14 copies K pages, warp 15 V pages
 constexpr int kThreads = 16 * 32;
-constexpr float kMaxSum = 256.f;           // a page's weights that sum to more move the row's reference
 }  // namespace one
 
 template <int D>
@@ -185,59 +295,7 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
             if (s < nst) copy_stage(s, ids[s]);
         next_ids = ids[STAGES];
     }
-    if (warp < kMmaWarp) {
-        // The Q tile, by warps 0-11: CL lanes share a row (a 16-byte chunk of 8
-        // values each, so the loads are coalesced and all of a thread's are in
-        // flight), find its largest magnitude by shuffles, and write the row as
-        // f16 -- once for every copy -- scaled by a power of two so that the
-        // copy of the bf16 values is exact.  A negative score scale goes into
-        // Q: the row's scale is >= 0.
-        constexpr int CL = D / 8, RPW = 32 / CL, NB0 = RT / (RPW * kMmaWarp) + 1;   // lanes per row, rows per warp and batch
-        const float sign = a.score_scale < 0.f ? -1.f : 1.f;
-        const int c = lane % CL;
-        uint4 qv[NB0];
-        auto row_of = [&](int i) { return (i * kMmaWarp + warp) * RPW + lane / CL; };   // row of the tile, batch i
-#pragma unroll
-        for (int i = 0; i < NB0; ++i) {
-            const int row = row_of(i), rr = u.R0 + row;
-            qv[i] = make_uint4(0, 0, 0, 0);
-            if (row < RT && rr < u.rows)
-                qv[i] = __ldg(reinterpret_cast<const uint4*>(
-                            a.q + (static_cast<int64_t>(u.q0 + (rr >> lg)) * a.num_q_heads + (hk << lg) +
-                                   (rr & ((1 << lg) - 1))) * D) + c);
-        }
-#pragma unroll
-        for (int i = 0; i < NB0; ++i) {
-            const int row = row_of(i);
-            const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-            float qmax = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                qmax = fmaxf(qmax, fmaxf(fabsf(bf16_to_f32(w4[e] & 0xFFFF)), fabsf(bf16_to_f32(w4[e] >> 16))));
-#pragma unroll
-            for (int off = CL / 2; off; off >>= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, off));
-            int shift = 0;
-            if (qmax > 0.f) {
-                const int e = static_cast<int>((__float_as_uint(qmax) >> 23) & 0xFF) - 127;
-                shift = max(-100, min(100, 14 - e));
-            }
-            const float up = sign * __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
-            uint32_t f[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                f[e] = pack_f16x2(bf16_to_f32(w4[e] & 0xFFFF) * up, bf16_to_f32(w4[e] >> 16) * up);
-            if (row < RT) {
-#pragma unroll
-                for (int o = 0; o < REP; ++o) {
-                    const int t = o * RT + row;
-                    *reinterpret_cast<uint4*>(sm + Og::QT + (c >> 3) * 16384 + t * 128 + (((c & 7) ^ (t & 7)) << 4)) =
-                        make_uint4(f[0], f[1], f[2], f[3]);
-                }
-                if (c == 0)
-                    row_scale[row] = fabsf(a.score_scale) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
-            }
-        }
-    }
+    if (warp < kMmaWarp) build_q_tiles<D, RT, REP, kMmaWarp>(a, u, hk, u.R0, sm + Og::QT, row_scale, warp, lane);
     if (warp == 0) tc::alloc(&tmem_base, Og::COLS);
     tc::fence_proxy_async_smem();  // the Q tile is read by the tensor cores
     tc::fence_before_sync();
@@ -274,7 +332,7 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
         auto wait_s = [&](int s) {
             return __all_sync(0xffffffffu, wait_or_abort(&s_full[s & 1], (s >> 1) & 1, a.wait_ns, abort_flag));
         };
-        // this copy's scores of stage s, HK at a time
+        // half h of this copy's scores of stage s (HK keys), masked
         float sv[HK];
         auto load = [&](int s, int h) {
             const uint32_t scol = trow + (s & 1) * KEYS + part * KP + HK * h;
@@ -283,6 +341,9 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
                 tc::ld32(scol + 32 * c, *reinterpret_cast<float(*)[32]>(sv + 32 * c));
 #pragma unroll
             for (int c = 0; c < HK / 32; ++c) tc::wait_ld(*reinterpret_cast<float(*)[32]>(sv + 32 * c));
+            const int t0 = (sp0 + s * PAGES) * kBS;
+            if (!(t0 + KEYS <= sp1 * kBS && t0 + KEYS - 1 <= wpos0 && t0 >= wlo1))
+                mask_keys<HK>(sv, t0 + part * KP + HK * h, lq, rv ? pq : -1, sp1 * kBS);
         };
         bool ok = true;
         if (NH == 1 && nst > 0) {
@@ -298,77 +359,23 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
             if (!__all_sync(0xffffffffu, wait_or_abort(&c_full[buf], (st >> 1) & 1, a.wait_ns, abort_flag))) break;
             if (warp_rows) {
                 if (NH > 1) tc::fence_after_sync();
-                const int pgs = sp0 + st * PAGES;
-                const int nk = min(PAGES, sp1 - pgs) * kBS;         // the stage's keys
-                const int t0 = pgs * kBS;
-                const bool interior = nk == KEYS && t0 + KEYS - 1 <= wpos0 && t0 >= wlo1;
+                const int t0 = (sp0 + st * PAGES) * kBS;
                 const uint32_t pcol = trow + Og::PC + buf * (KEYS / 2) + part * (KP / 2);  // this copy's P, two keys a column
                 const float4* scale = psc[buf] + part * (KP / kBS);
-                auto key_ok = [&](int jj) {   // jj: key of the stage
-                    const int key = t0 + jj;
-                    return jj < nk && rv && key >= lq && key <= pq;
-                };
-                // The part's weights under the reference maximum m, into P;
-                // their sum over the V scales, and the largest sum of a page's.
                 float ls, top = 0.f;
-                auto weigh = [&]() {
-                    ls = 0.f;
-                    top = 0.f;
-                    const float nmuse = m == -INFINITY ? 0.f : -m;
-#pragma unroll 1
-                    for (int h = 0; h < NH; ++h) {
-                        if constexpr (NH > 1) load(st, h);
-#pragma unroll
-                        for (int p2 = 0; p2 < HK / 32; ++p2) {   // two pages: 16 columns of P
-                            float pw[16];
-#pragma unroll
-                            for (int pp = 0; pp < 2; ++pp) {
-                                const int page = 2 * p2 + pp;
-                                const float4 w = scale[HK / kBS * h + page];
-                                const float c = cs * w.x, n = w.y + nmuse;
-                                float ps[2] = {0.f, 0.f};
-                                if (interior) {
-#pragma unroll
-                                    for (int i = 0; i < kBS / 2; ++i) {   // key pairs in packed FP32 pairs
-                                        const int j = kBS * page + 2 * i;
-                                        float x0, x1;
-                                        fma_f32x2(x0, x1, sv[j], sv[j + 1], c, c, n, n);
-                                        const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                                        add_f32x2(ps[0], ps[1], p0, p1);
-                                        pw[8 * pp + i] = __uint_as_float(pack_f16x2(p0, p1));
-                                    }
-                                } else {
-#pragma unroll
-                                    for (int i = 0; i < kBS / 2; ++i) {   // masked keys weigh 0 (also when cs = 0)
-                                        const int j = kBS * page + 2 * i, jj = part * KP + HK * h + j;
-                                        const float p0 = key_ok(jj) ? fast_exp2(fmaf(sv[j], c, n)) : 0.f;
-                                        const float p1 = key_ok(jj + 1) ? fast_exp2(fmaf(sv[j + 1], c, n)) : 0.f;
-                                        ps[0] += p0;
-                                        ps[1] += p1;
-                                        pw[8 * pp + i] = __uint_as_float(pack_f16x2(p0, p1));
-                                    }
-                                }
-                                const float sum = ps[0] + ps[1];
-                                ls = fmaf(sum, w.z, ls);
-                                top = fmaxf(top, sum);
-                            }
-                            tc::st16(pcol + HK / 2 * h + 16 * p2, pw);
-                        }
-                    }
-                };
                 // First under the reference the row has, which mostly still
                 // holds: the scores are read once and no maximum is looked for.
                 // A row's first keys, or a page whose weights sum to more than
                 // 2^8 (no weight of a smaller sum is above it, so all are f16),
                 // send the warp the long way.
-                const int k0 = t0 + part * KP, k1 = min(t0 + nk, k0 + KP) - 1;
+                const int k0 = t0 + part * KP, k1 = min(sp1 * kBS, k0 + KP) - 1;
                 bool look = __any_sync(0xffffffffu, m == -INFINITY && rv && pq >= k0 && lq <= k1 && k0 <= k1);
 #pragma unroll 1
                 while (true) {
                     if (look) {
                         // page by page (from tensor memory again, in a loop:
                         // this path is rare and should be small): the largest
-                        // raw score, scaled (cs and the K scale are >= 0),
+                        // raw score, scaled (cs and the K scale are > 0),
                         // plus the V scale's logarithm
                         float mx = -INFINITY;
 #pragma unroll 1
@@ -376,10 +383,11 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
                             float x[16], big = -INFINITY;
                             tc::ld16(trow + buf * KEYS + part * KP + kBS * pg, x);
                             tc::wait_ld(x);
+                            mask_keys<16>(x, k0 + kBS * pg, lq, rv ? pq : -1, sp1 * kBS);
 #pragma unroll
-                            for (int i = 0; i < kBS; ++i) big = fmaxf(big, key_ok(part * KP + kBS * pg + i) ? x[i] : -INFINITY);
+                            for (int i = 0; i < kBS; ++i) big = fmaxf(big, x[i]);
                             const float4 w = scale[pg];
-                            mx = fmaxf(mx, big == -INFINITY ? -INFINITY : fmaf(big, cs * w.x, w.y));
+                            mx = fmaxf(mx, fmaf(big, cs * w.x, w.y));
                         }
                         // such a row's reference moves to its maximum; a row that
                         // had none (m = -inf) holds O = 0 and l = 0
@@ -409,7 +417,12 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
                             }
                         }
                     }
-                    weigh();
+                    ls = top = 0.f;
+#pragma unroll 1
+                    for (int h = 0; h < NH; ++h) {
+                        if constexpr (NH > 1) load(st, h);
+                        weigh_keys<HK>(sv, scale + HK / kBS * h, cs, m, pcol + HK / 2 * h, ls, top);
+                    }
                     if (look) break;
                     look = __any_sync(0xffffffffu, top > kMaxSum);
                     if (!look) break;
