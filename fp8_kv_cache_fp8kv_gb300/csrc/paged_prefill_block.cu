@@ -631,6 +631,409 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
     }
 }
 
+// ---------------------------------------------------------------------------
+// The two-tile kernel (d = 64 and 128, chunks of at least two tiles): 256 query
+// rows of one (sequence, kv head) per CTA, so that each stage's operand tiles
+// serve two tiles, in stages of 64 keys.
+//
+// Roles, each of which keeps a ring ahead of the next:
+//   * warps 8-11 copy and convert K, warps 12-15 V (transposed): cp.async two
+//     stages ahead into a ring of their own (a barrier of the four warps tells
+//     that a stage has landed and that the slot to refill has been read), block
+//     ids a stage ahead of that, then the conversion into one of two operand
+//     tiles;
+//   * one thread of warp 16 issues the MMAs.  Tile by tile: once P of stage s is
+//     in, O += P V, then S = Q K^T of stage s + 2 into the buffer that held P(s)
+//     (the MMAs of one thread run in issue order).  S has two buffers per tile,
+//     so a tile's next scores are there when its softmax is done;
+//   * warp 17 prepares the page scales, a stage ahead;
+//   * warps 0-3 and 4-7 (a warpgroup per tile, thread = row = TMEM lane) weigh
+//     the stage as the one-tile kernel does -- under the reference the row has,
+//     one read of S, P over the S just read -- and read the next stage's scores
+//     before they hand P over.
+// A 64-key stage halves what a row holds in registers against 128 keys, which is
+// what lets it be read once; the tensor cores lose little (N = 64 for S).
+namespace two {
+constexpr int kTiles = 2;
+constexpr int kKWarp0 = 8, kVWarp0 = 12;   // warps 8-11 convert K, 12-15 V
+constexpr int kMmaWarp = 16, kScaleWarp = 17;
+constexpr int kThreads = 20 * 32;          // (warps 18 and 19 fill the last warpgroup)
+// Registers a thread: launched with kRegs, then shared out by warpgroup -- the
+// softmax holds 64 scores.  The shares add up to the launch's total, or less,
+// so that every increase is granted.
+constexpr int kRegs = 96, kSoftRegs = 112, kConvRegs = 96, kAuxRegs = 64;
+static_assert(2 * kSoftRegs + 2 * kConvRegs + kAuxRegs <= 5 * kRegs, "register shares");
+constexpr int kBar = 2;                    // named barriers of the converter groups: 2 (K), 3 (V)
+constexpr int kStg = 3;                    // stages in a staging ring
+}  // namespace two
+
+template <int D>
+struct TwoGeo {
+    static constexpr int KEYS = tcg::kKeys, PAGES = KEYS / kBS;
+    static constexpr int QTB = D / 64 * 128 * 128;      // one Q tile: 128 rows x d
+    static constexpr int KTB = D / 64 * KEYS * 128;     // a K tile: 64 keys x d
+    static constexpr int VTB = D * 128;                 // a V^T tile: d rows x 64 keys
+    static constexpr int SLOT = KEYS * D;               // one staging slot: 64 fp8 rows
+    static constexpr int QT = 0, KT = QT + two::kTiles * QTB, VT = KT + 2 * KTB, STG = VT + 2 * VTB;
+    static constexpr int SMEM = STG + 2 * two::kStg * SLOT;   // 176 KB at d = 128, 88 KB at 64
+    // TMEM columns per tile: two S buffers (P over the first half of each), then O
+    static constexpr uint32_t OC = 2 * KEYS, TC = 256, COLS = two::kTiles * TC;
+    static_assert(OC + D <= TC, "TMEM columns");
+};
+
+template <int N>
+__device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+template <int D>
+__global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(const Args a) {
+    using namespace two;
+    using Tg = TwoGeo<D>;
+    constexpr int KEYS = Tg::KEYS, PAGES = Tg::PAGES;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], c_full[2], c_empty[2];
+    __shared__ uint64_t s_full[kTiles][2], p_full[kTiles][2], done_bar;
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_sh;
+    __shared__ float4 psc[2][PAGES];
+    __shared__ float row_scale[kTiles * 128];
+    volatile int* abort_flag = &abort_sh;
+    uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    const uint32_t sb = smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int j = 0; j < 2; ++j) {
+            mbar_init(&k_full[j], 128);
+            mbar_init(&k_empty[j], 1);     // tcgen05.commit
+            mbar_init(&v_full[j], 128);
+            mbar_init(&v_empty[j], 1);
+            mbar_init(&c_full[j], 1);      // the scale warp
+            mbar_init(&c_empty[j], 8);     // the softmax warps
+            for (int i = 0; i < kTiles; ++i) {
+                mbar_init(&s_full[i][j], 1);
+                mbar_init(&p_full[i][j], 128);
+            }
+        }
+        mbar_init(&done_bar, 1);
+        abort_sh = 0;
+        fence_barrier_init();
+    }
+    griddep_wait();                // inputs may come from the previous grid on the stream
+    griddep_launch_dependents();
+    const int b = blockIdx.z, hk = blockIdx.y;
+    const int pair = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
+    Unit u, u1;
+    if (!make_unit<0>(a, b, 2 * pair, blockIdx.x == 0 && hk == 0 && tid == 0, u)) return;
+    const bool has1 = make_unit<0>(a, b, 2 * pair + 1, false, u1);
+    const int lg = a.log2_group;
+    // the pair's keys: the first tile's window starts first, the second tile's rows end last
+    const int kmin = u.kmin, kmax = has1 ? u1.kmax : u.kmax;
+    const int pg0 = kmin / kBS, np_all = kmax / kBS - pg0 + 1;
+    const int sp0 = pg0 + static_cast<int>(static_cast<int64_t>(split) * np_all / a.splits);
+    const int sp1 = pg0 + static_cast<int>(static_cast<int64_t>(split + 1) * np_all / a.splits);
+    const int nst = (sp1 - sp0 + PAGES - 1) / PAGES;
+    const int32_t* bt = a.block_tables + static_cast<int64_t>(b) * a.max_blocks_per_seq;
+
+    // ---- set-up: the converters start the first stages' copies, then warps
+    // 0-15 build the Q tiles
+    const bool is_v = warp >= kVWarp0;            // (of warps 8-15)
+    const int ct = tid & 127;                     // thread within its group of four warps
+    // Stage s's block ids, lane p holding page p's as the table has it (looking
+    // at it here would wait for the read).
+    auto blocks_of = [&](int s) {
+        const int pg = sp0 + s * PAGES + lane;
+        return lane < PAGES && pg < sp1 ? __ldg(bt + pg) : 0;
+    };
+    auto copy_stage = [&](int s, int ids) {       // one commit group per stage, also an empty one
+        const int np = sp1 - sp0 - s * PAGES;     // pages left (<= 0 past the range)
+        if (ids < 0 || ids >= a.num_blocks) {     // block 0 is read instead
+            report(a.err, FP8KV_ERR_INVALID_ARG);
+            ids = 0;
+        }
+        const uint8_t* cache = is_v ? a.v_cache : a.k_cache;
+        const uint32_t dst = sb + Tg::STG + ((is_v ? kStg : 0) + s % kStg) * Tg::SLOT;
+        constexpr int CPR = D / 16, CPP = kBS * CPR;   // 16-byte chunks per row, per page
+#pragma unroll
+        for (int it = 0; it < PAGES * CPP / 128; ++it) {
+            const int i = ct + it * 128, p = i / CPP, ci = i % CPP;   // p is the same for a warp
+            const int id = __shfl_sync(0xffffffffu, ids, p);
+            if (p < np) {
+                const int k = p * kBS + ci / CPR, c = ci % CPR;
+                cp_async16(dst + (is_v ? stg_v<D>(k, c) : stg_k<D>(k, c)),
+                           cache + (static_cast<int64_t>(id) * a.num_kv_heads + hk) * (kBS * D) + ci * 16);
+            }
+        }
+        cp_async_commit();
+    };
+    int next_ids = 0;
+    if (warp >= kKWarp0 && warp < kMmaWarp) {
+        const int id0 = blocks_of(0), id1 = blocks_of(1);
+        next_ids = blocks_of(2);
+        copy_stage(0, id0);
+        copy_stage(1, id1);
+    }
+    if (warp < kMmaWarp)
+        build_q_tiles<D, kTiles * 128, 1, kMmaWarp>(a, u, hk, u.R0, sm + Tg::QT, row_scale, warp, lane);
+    if (warp == 0) tc::alloc(&tmem_base, Tg::COLS);
+    tc::fence_proxy_async_smem();  // the Q tiles are read by the tensor cores
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tm = tmem_base;
+
+    const int ti = warp >> 2;                     // the tile of warps 0-7
+    const int r = u.R0 + tid;                     // its row (the tiles' rows are consecutive)
+    const bool rv = warp < 8 && r < u.rows;
+    const uint32_t trow = tm + (ti & 1) * Tg::TC + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    float m = -INFINITY, l = 0.f;
+    if (warp < 8) {
+        // ---------------------------------------------------------- softmax of tile ti
+        more_regs<kSoftRegs>();
+        const float cs = row_scale[tid];
+        const int pq = rv ? u.L - u.n + (r >> lg) : -1;
+        const int lq = (a.window > 0 && pq + 1 > a.window) ? pq + 1 - a.window : 0;
+        // the warp's first position and its last valid row's window start: a
+        // stage of keys in [wlo1, wpos0] is attended in full by every row of the warp
+        const int wr0 = u.R0 + warp * 32;
+        const int wpos0 = u.L - u.n + (wr0 >> lg);
+        const int wpos1 = u.L - u.n + (max(0, min(wr0 + 31, u.rows - 1)) >> lg);
+        const int wlo1 = (a.window > 0 && wpos1 + 1 > a.window) ? wpos1 + 1 - a.window : 0;
+        const bool warp_rows = wr0 < u.rows;      // a warp of no rows only keeps the handshake
+        {
+            float z[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) z[j] = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) tc::st32(trow + Tg::OC + 32 * c, z);
+            tc::wait_st();
+        }
+        // (the waits' results are made warp-uniform: the TMEM loads are collective)
+        auto wait_s = [&](int s) {
+            return __all_sync(0xffffffffu, wait_or_abort(&s_full[ti][s & 1], (s >> 1) & 1, a.wait_ns, abort_flag));
+        };
+        float sv[KEYS];
+        auto load = [&](int s) {                  // the row's scores of stage s, masked
+            const uint32_t scol = trow + (s & 1) * KEYS;
+            tc::fence_after_sync();
+            tc::ld32(scol, *reinterpret_cast<float(*)[32]>(sv));
+            tc::ld32(scol + 32, *reinterpret_cast<float(*)[32]>(sv + 32));
+            tc::wait_ld(*reinterpret_cast<float(*)[32]>(sv));
+            tc::wait_ld(*reinterpret_cast<float(*)[32]>(sv + 32));
+            const int t0 = (sp0 + s * PAGES) * kBS;
+            if (!(t0 + KEYS <= sp1 * kBS && t0 + KEYS - 1 <= wpos0 && t0 >= wlo1))
+                mask_keys<KEYS>(sv, t0, lq, pq, sp1 * kBS);
+        };
+        bool ok = nst == 0 || wait_s(0);
+        if (ok && nst > 0 && warp_rows) load(0);
+        for (int st = 0; st < nst && ok; ++st) {
+            const int buf = st & 1;
+            if (!__all_sync(0xffffffffu, wait_or_abort(&c_full[buf], (st >> 1) & 1, a.wait_ns, abort_flag))) break;
+            if (warp_rows) {
+                const int t0 = (sp0 + st * PAGES) * kBS;
+                const float4* scale = psc[buf];
+                float ls, top = 0.f;
+                // as in the one-tile kernel: under the reference the row has, or
+                // the long way for its first keys and for a page that outgrows it
+                bool look = __any_sync(0xffffffffu, m == -INFINITY && pq >= t0 && lq < min(t0 + KEYS, sp1 * kBS));
+#pragma unroll 1
+                while (true) {
+                    if (look) {
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int pg = 0; pg < PAGES; ++pg) {
+                            float big = -INFINITY;
+#pragma unroll
+                            for (int i = 0; i < kBS; ++i) big = fmaxf(big, sv[kBS * pg + i]);
+                            const float4 w = scale[pg];
+                            mx = fmaxf(mx, fmaf(big, cs * w.x, w.y));
+                        }
+                        const float mn = fmaxf(m, mx);
+                        const bool upd = mn > m && (m == -INFINITY || top > kMaxSum);
+                        const bool held = upd && m != -INFINITY;
+                        float alpha = 1.f;
+                        if (upd) {
+                            alpha = fast_exp2(m - mn);
+                            l *= alpha;
+                            m = mn;
+                        }
+                        if (__any_sync(0xffffffffu, held)) {
+                            // O = O * alpha for the warp's rows, once the value MMAs of stage st - 1 are in
+                            ok = __all_sync(0xffffffffu, wait_or_abort(&v_empty[buf ^ 1], ((st - 1) >> 1) & 1, a.wait_ns,
+                                                                       abort_flag));
+                            if (!ok) break;
+                            tc::fence_after_sync();
+#pragma unroll 1
+                            for (int c = 0; c < D / 16; ++c) {   // (16 at a time: the scores are in registers)
+                                float x[16];
+                                tc::ld16(trow + Tg::OC + 16 * c, x);
+                                tc::wait_ld(x);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) x[j] *= alpha;
+                                tc::st16(trow + Tg::OC + 16 * c, x);
+                            }
+                        }
+                    }
+                    ls = top = 0.f;
+                    weigh_keys<KEYS>(sv, scale, cs, m, trow + buf * KEYS, ls, top);
+                    if (look) break;
+                    look = __any_sync(0xffffffffu, top > kMaxSum);
+                    if (!look) break;
+                }
+                if (!ok) break;
+                l += ls;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c_empty[buf]);
+            if (st + 1 < nst) {
+                // the next stage's scores move to registers before P is handed
+                // over: a load would wait for the value MMAs, which then run
+                ok = wait_s(st + 1);
+                if (!ok) break;
+                if (warp_rows) load(st + 1);
+            }
+            if (warp_rows) {
+                tc::wait_st();
+                tc::fence_before_sync();
+            }
+            mbar_arrive(&p_full[ti][buf]);     // P (and the rescaled O) are in TMEM
+        }
+    } else if (warp < kMmaWarp) {
+        // ---------------------------------------------------------- converters of K or of V
+        fewer_regs<kConvRegs>();
+        const int bar = kBar + (is_v ? 1 : 0);
+        uint64_t* full = is_v ? v_full : k_full;
+        uint64_t* empty = is_v ? v_empty : k_empty;
+        bool ok = true;
+        for (int st = 0; st < nst; ++st) {
+            cp_async_wait<1>();                // this thread's copies of stage st have landed
+            // everyone's have; the slot of stage st - 1 has been read (or all give up)
+            if (named_bar_or(bar, 128, !ok)) break;
+            copy_stage(st + 2, next_ids);
+            next_ids = blocks_of(st + 3);
+            const int j = st & 1;
+            // tile j is free once the MMAs of stage st - 2 that read it have completed
+            ok = st < 2 || wait_or_abort(&empty[j], ((st >> 1) + 1) & 1, a.wait_ns, abort_flag);
+            if (!ok) continue;                 // (to the barrier, where the group leaves together)
+            const int pg = sp0 + st * PAGES;
+            if (is_v) {
+                // (the conversion's V rows follow 64 K rows in its source)
+                convert_stage_v<D>(sm + Tg::STG + (kStg + st % kStg) * Tg::SLOT - tcg::kKeys * D,
+                                   sm + Tg::VT + j * Tg::VTB, ct, pg * kBS, min(PAGES, sp1 - pg), kmin, kmax);
+            } else {
+                convert_stage_k<D>(sm + Tg::STG + st % kStg * Tg::SLOT, sm + Tg::KT + j * Tg::KTB, ct);
+            }
+            tc::fence_proxy_async_smem();      // the tile is read by the tensor cores
+            mbar_arrive(&full[j]);
+        }
+        cp_async_wait<0>();                    // no copy lands after the CTA is gone
+    } else {
+    fewer_regs<kAuxRegs>();
+    if (warp == kScaleWarp) {
+        // ---------------------------------------------------------- page scales
+        PageScales<PAGES> feed(a, bt, hk, sp0, sp1, lane);
+        for (int st = 0; st < nst; ++st) {
+            if (st >= 2 && !__all_sync(0xffffffffu, wait_or_abort(&c_empty[st & 1], ((st >> 1) + 1) & 1, a.wait_ns,
+                                                                  abort_flag)))
+                break;
+            feed.write(psc[st & 1]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c_full[st & 1]);
+            feed.advance(sp0 + st * PAGES);
+        }
+    } else if (warp == kMmaWarp && lane == 0) {
+        // ---------------------------------------------------------- MMA issuer
+        constexpr uint32_t id_s = tc::idesc_f16_f32(128, KEYS);
+        constexpr uint32_t id_o = tc::idesc_f16_f32(128, D);
+        const bool stall_cta = blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0;
+        // S = Q K^T of stage s for tile i into the stage's buffer
+        auto issue_s = [&](int i, int s) {
+            if (i == 0) {
+                if (!wait_or_abort(&k_full[s & 1], (s >> 1) & 1, a.wait_ns, abort_flag)) return false;
+                tc::fence_after_sync();
+            }
+            if (!(s == a.stall_stage && stall_cta)) {   // test hook: this stage's S never arrives
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = (ks & 3) * 32;
+                    tc::mma_f16(tm + i * Tg::TC + (s & 1) * KEYS,
+                                tc::desc_k_sw128(sb + Tg::QT + i * Tg::QTB + (ks >> 2) * 16384 + off),
+                                tc::desc_k_sw128(sb + Tg::KT + (s & 1) * Tg::KTB + (ks >> 2) * (KEYS * 128) + off), id_s,
+                                ks > 0);
+                }
+                tc::commit(&s_full[i][s & 1]);
+            }
+            if (i == kTiles - 1) tc::commit(&k_empty[s & 1]);   // the K tile is free when the score MMAs complete
+            return true;
+        };
+        bool ok = true;
+        for (int s = 0; s < 2 && s < nst && ok; ++s)
+            for (int i = 0; i < kTiles && ok; ++i) ok = issue_s(i, s);
+        for (int st = 0; st < nst && ok; ++st)
+            for (int i = 0; i < kTiles && ok; ++i) {
+                const int buf = st & 1;
+                ok = wait_or_abort(&p_full[i][buf], (st >> 1) & 1, a.wait_ns, abort_flag) &&
+                     (i > 0 || wait_or_abort(&v_full[buf], (st >> 1) & 1, a.wait_ns, abort_flag));
+                if (!ok) break;
+                tc::fence_after_sync();
+                // O += P V: P (128 rows x 64 keys) from the first half of the stage's S columns
+#pragma unroll
+                for (int ks = 0; ks < KEYS / 16; ++ks)
+                    tc::mma_f16_ts(tm + i * Tg::TC + Tg::OC, tm + i * Tg::TC + buf * KEYS + ks * 8,
+                                   tc::desc_k_sw128(sb + Tg::VT + buf * Tg::VTB + ks * 32), id_o, 1);
+                // the V^T tile is free, and both O complete, when both tiles' value MMAs complete
+                if (i == kTiles - 1) tc::commit(&v_empty[buf]);
+                if (st + 2 < nst) ok = issue_s(i, st + 2);
+            }
+        // every MMA this thread issued completes before TMEM is released
+        tc::commit(&done_bar);
+        mbar_wait_bounded(&done_bar, 0, tcg::kWaitNs);
+    }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const bool failed = *abort_flag != 0;
+    if (failed) {
+        if (tid == 0) report(a.err, FP8KV_ERR_TIMEOUT);
+    } else if (warp < 8) {
+        // ---- the rows' outputs (or partials) from the TMEM accumulator; every
+        // thread of the warp loads (tcgen05.ld is collective), valid rows store
+        const int64_t unit = (static_cast<int64_t>(b) * a.num_kv_heads + hk) * a.tiles + 2 * pair + ti;
+        const float so = l > 0.f ? 1.f / l : 0.f;
+        uint4* orow = reinterpret_cast<uint4*>(
+            a.out + (static_cast<int64_t>(u.q0 + (rv ? r >> lg : 0)) * a.num_q_heads + (hk << lg) +
+                     (rv ? r & ((1 << lg) - 1) : 0)) * D);
+        const int64_t slot = (unit * a.splits + split) * a.rows + (tid & 127);
+        float4* po = reinterpret_cast<float4*>(a.part_o + slot * D);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+            float x[32];
+            tc::ld32(trow + Tg::OC + 32 * c, x);
+            tc::wait_ld(x);
+            if (!rv) continue;
+            if (a.splits == 1) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    orow[4 * c + i] = make_uint4(pack_bf16x2(x[8 * i] * so, x[8 * i + 1] * so),
+                                                 pack_bf16x2(x[8 * i + 2] * so, x[8 * i + 3] * so),
+                                                 pack_bf16x2(x[8 * i + 4] * so, x[8 * i + 5] * so),
+                                                 pack_bf16x2(x[8 * i + 6] * so, x[8 * i + 7] * so));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) po[8 * c + i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            }
+        }
+        if (rv && a.splits > 1) a.part_ml[slot] = make_float2(m, l);
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 0) {
+        tc::fence_after_sync();
+        tc::dealloc(tm, Tg::COLS);
+    }
+}
+
 // ---------------------------------------------------------------- launch
 
 // Launches `kernel` with programmatic launch; raises its dynamic
@@ -686,9 +1089,15 @@ static cudaError_t launch_block_g(int kind, const Args& a, int batch, cudaStream
     } else {
         if constexpr (D < 256) {
             static std::atomic<uint64_t> done{0};
-            const int pairs = (a.tiles + ws::kTiles - 1) / ws::kTiles;
-            e = launch_with(paged_prefill_ws_kernel<D, G, true>, done, static_cast<size_t>(WsGeo<D>::SMEM) + 1024,
-                            dim3(static_cast<unsigned>(pairs * a.splits), hkv, bz), ws::kThreads, a, s);
+            // the register shares rest on the launch's total
+            static const bool regs_ok = [] {
+                cudaFuncAttributes at;
+                return cudaFuncGetAttributes(&at, paged_prefill_two_kernel<D>) == cudaSuccess && at.numRegs >= two::kRegs;
+            }();
+            if (!regs_ok) return cudaErrorInvalidConfiguration;
+            const int pairs = (a.tiles + two::kTiles - 1) / two::kTiles;
+            e = launch_with(paged_prefill_two_kernel<D>, done, static_cast<size_t>(TwoGeo<D>::SMEM) + 1024,
+                            dim3(static_cast<unsigned>(pairs * a.splits), hkv, bz), two::kThreads, a, s);
         }
     }
     if (e != cudaSuccess || a.splits == 1) return e;
