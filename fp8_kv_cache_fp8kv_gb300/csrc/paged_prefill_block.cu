@@ -497,17 +497,17 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
         constexpr uint32_t id_s = tc::idesc_f16_f32(128, KEYS);
         constexpr uint32_t id_o = tc::idesc_f16_f32(128, D);
         const bool stall_cta = blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0;
+        const uint64_t qd = tc::desc_k_sw128(sb + Og::QT), kd = tc::desc_k_sw128(sb + Og::KT),
+                       vd0 = tc::desc_k_sw128(sb + Og::VT);
         // S = Q K^T of stage s into its buffer
         auto issue_s = [&](int s) {
             if (!wait_or_abort(&k_full, s & 1, a.wait_ns, abort_flag)) return false;
             tc::fence_after_sync();
             if (!(s == a.stall_stage && stall_cta)) {   // test hook: this stage's S never arrives
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = (ks & 3) * 32;
-                    tc::mma_f16(tm + (s & 1) * KEYS, tc::desc_k_sw128(sb + Og::QT + (ks >> 2) * 16384 + off),
-                                tc::desc_k_sw128(sb + Og::KT + (ks >> 2) * Og::KAT + off), id_s, ks > 0);
-                }
+                for (int ks = 0; ks < D / 16; ++ks)
+                    tc::mma_f16(tm + (s & 1) * KEYS, tc::desc_at(qd, (ks >> 2) * 16384 + (ks & 3) * 32),
+                                tc::desc_at(kd, (ks >> 2) * Og::KAT + (ks & 3) * 32), id_s, ks > 0);
                 tc::commit(&s_full[s & 1]);
             }
             tc::commit(&k_empty);                // the K tile is free when the score MMAs complete
@@ -521,11 +521,11 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
                 break;
             tc::fence_after_sync();
             // O += P V: P (128 rows x KEYS) from tensor memory
+            const uint32_t pc = tm + Og::PC + (st & 1) * (KEYS / 2);
+            const uint64_t vd = tc::desc_at(vd0, (st & 1) * Og::VTB);
 #pragma unroll
             for (int ks = 0; ks < KEYS / 16; ++ks)
-                tc::mma_f16_ts(tm + Og::OC, tm + Og::PC + (st & 1) * (KEYS / 2) + ks * 8,
-                               tc::desc_k_sw128(sb + Og::VT + (st & 1) * Og::VTB + (ks >> 2) * Og::VAT + (ks & 3) * 32),
-                               id_o, 1);
+                tc::mma_f16_ts(tm + Og::OC, pc + ks * 8, tc::desc_at(vd, (ks >> 2) * Og::VAT + (ks & 3) * 32), id_o, 1);
             tc::commit(&v_empty[st & 1]);        // the V^T tile is free, and O complete, when the value MMAs complete
         }
         // every MMA this thread issued completes before TMEM is released
@@ -946,21 +946,21 @@ __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(con
         constexpr uint32_t id_s = tc::idesc_f16_f32(128, KEYS);
         constexpr uint32_t id_o = tc::idesc_f16_f32(128, D);
         const bool stall_cta = blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0;
+        const uint64_t qd0 = tc::desc_k_sw128(sb + Tg::QT), kd0 = tc::desc_k_sw128(sb + Tg::KT),
+                       vd0 = tc::desc_k_sw128(sb + Tg::VT);
         // S = Q K^T of stage s for tile i into the stage's buffer
         auto issue_s = [&](int i, int s) {
             if (i == 0) {
                 if (!wait_or_abort(&k_full[s & 1], (s >> 1) & 1, a.wait_ns, abort_flag)) return false;
                 tc::fence_after_sync();
             }
+            const uint32_t sc = tm + i * Tg::TC + (s & 1) * KEYS;
+            const uint64_t qd = tc::desc_at(qd0, i * Tg::QTB), kd = tc::desc_at(kd0, (s & 1) * Tg::KTB);
             if (!(s == a.stall_stage && stall_cta)) {   // test hook: this stage's S never arrives
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = (ks & 3) * 32;
-                    tc::mma_f16(tm + i * Tg::TC + (s & 1) * KEYS,
-                                tc::desc_k_sw128(sb + Tg::QT + i * Tg::QTB + (ks >> 2) * 16384 + off),
-                                tc::desc_k_sw128(sb + Tg::KT + (s & 1) * Tg::KTB + (ks >> 2) * (KEYS * 128) + off), id_s,
-                                ks > 0);
-                }
+                for (int ks = 0; ks < D / 16; ++ks)
+                    tc::mma_f16(sc, tc::desc_at(qd, (ks >> 2) * 16384 + (ks & 3) * 32),
+                                tc::desc_at(kd, (ks >> 2) * (KEYS * 128) + (ks & 3) * 32), id_s, ks > 0);
                 tc::commit(&s_full[i][s & 1]);
             }
             if (i == kTiles - 1) tc::commit(&k_empty[s & 1]);   // the K tile is free when the score MMAs complete
@@ -977,10 +977,11 @@ __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(con
                 if (!ok) break;
                 tc::fence_after_sync();
                 // O += P V: P (128 rows x 64 keys) from the first half of the stage's S columns
+                const uint32_t oc = tm + i * Tg::TC + Tg::OC;
+                const uint64_t vd = tc::desc_at(vd0, buf * Tg::VTB);
 #pragma unroll
                 for (int ks = 0; ks < KEYS / 16; ++ks)
-                    tc::mma_f16_ts(tm + i * Tg::TC + Tg::OC, tm + i * Tg::TC + buf * KEYS + ks * 8,
-                                   tc::desc_k_sw128(sb + Tg::VT + buf * Tg::VTB + ks * 32), id_o, 1);
+                    tc::mma_f16_ts(oc, oc - Tg::OC + buf * KEYS + ks * 8, tc::desc_at(vd, ks * 32), id_o, 1);
                 // the V^T tile is free, and both O complete, when both tiles' value MMAs complete
                 if (i == kTiles - 1) tc::commit(&v_empty[buf]);
                 if (st + 2 < nst) ok = issue_s(i, st + 2);

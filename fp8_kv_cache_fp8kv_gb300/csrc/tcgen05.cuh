@@ -32,6 +32,15 @@ __device__ __forceinline__ uint64_t desc_k_sw128(uint32_t saddr) {
     return d;
 }
 
+// The descriptor of the operand `bytes` (a multiple of 16) further on: the
+// start-address field does not overflow below 256 KB, so one 32-bit addition.
+// Building each MMA's descriptors anew costs the issuing thread about 100
+// cycles an MMA, more than the MMA itself.
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) {
+    const uint32_t lo = static_cast<uint32_t>(desc) + (bytes >> 4);
+    return (desc & 0xFFFFFFFF00000000ull) | lo;
+}
+
 // Instruction descriptor of kind::f16 with f16 A and B, an FP32 accumulator
 // and both operands K-major (bits: D format 1 = F32 in [4,6), A and B
 // format 0 = F16 in [7,10) and [10,13), N >> 3 in [17,23), M >> 4 in [24,29)).
