@@ -2,19 +2,76 @@
 // scale for every (page, kv head), the granularity below the per-tensor and
 // per-head scales of gpusmith.com, "FP8 KV Cache Quantization: Capacity Gains
 // and Accuracy Risk", "Scales and calibration".  How the scales enter the
-// softmax is described at PageScales (prefill_kernels.cuh).
+// softmax is described at PageScales (prefill_common.cuh).
 //
-// Chunks of several query tiles at d = 64 and 128 run the two-tile kernel of
-// the per-tensor call with BS = true.  Everything else -- d = 256, and chunks
-// of at most 128 query rows (drafted tokens being checked, short turns) -- runs
-// the one-tile kernel below.
-#include "prefill_kernels.cuh"
+// Two kernels on the 5th-generation tensor cores: chunks of several query tiles
+// at d = 64 and 128 run the two-tile kernel, everything else -- d = 256, and
+// chunks of at most 128 query rows (drafted tokens being checked, short turns)
+// -- the one-tile kernel.
+//
+// How the scales enter the softmax.  With c_t the codes and ks, vs the scales of
+// key t's page, in log2 units:
+//     score  s_t = x_t (cs ks),   x_t the raw score q . ck_t,
+//     weight w_t = 2^(s_t + log2 vs - m),
+//     O = sum_t w_t cv_t,   l = sum_t w_t / vs,   out = O / l.
+// The V scale goes into the exponent, where it costs nothing: it is the addend
+// of the FMA that applies the score multiplier, one multiplier and one addend
+// per page of 16 keys.  m refers to s + log2 vs, so weights stay small however
+// the scales differ, and a weight is rounded to f16 relative to the largest in
+// the sum it enters.  The row sum takes each page's weights times 1 / vs, in
+// FP32.
+#include <cuda_fp16.h>
+
+#include "prefill_common.cuh"
 
 namespace fp8kv {
 namespace prefill {
 
 // ---------------------------------------------------------------------------
 // What the two kernels share.
+
+// A range's page scales, read by one warp: lane p < PAGES holds page p of a
+// stage, its scales one stage ahead and its block id two.
+template <int PAGES>
+struct PageScales {
+    const Args& a;
+    const int32_t* bt;   // the sequence's block-table row
+    int hk, end, lane;   // kv head; first page past the range
+    int id;              // block of the page of the stage after next, as the table has it
+    float k, v;          // next stage's scales
+
+    // The id as the table has it: looking at it here would wait for the read.
+    __device__ __forceinline__ int block_of(int pg) const {
+        return lane < PAGES && pg + lane < end ? __ldg(bt + pg + lane) : 0;
+    }
+    // The scales of the pages at pg, whose ids are held; 1 past the range.  A
+    // bad id reads block 0's, as the copies do (they report it).
+    __device__ __forceinline__ void fetch(int pg) {
+        k = v = 1.f;
+        if (lane < PAGES && pg + lane < end) {
+            const int64_t b = id >= 0 && id < a.num_blocks ? id : 0;
+            k = __ldg(a.k_page_scales + b * a.num_kv_heads + hk);
+            v = __ldg(a.v_page_scales + b * a.num_kv_heads + hk);
+        }
+    }
+    // Starts the reads of the stage at page pg and of the block ids after it.
+    __device__ __forceinline__ PageScales(const Args& args, const int32_t* row, int head, int pg, int past, int ln)
+        : a(args), bt(row), hk(head), end(past), lane(ln) {
+        id = block_of(pg);
+        fetch(pg);
+        id = block_of(pg + PAGES);
+    }
+    // The stage's entries into the table.
+    __device__ __forceinline__ void write(float4* table) const {
+        if (lane < PAGES) table[lane] = make_float4(k, log2f(v), 1.f / v, 0.f);
+    }
+    // The reads move on from the stage at page pg.
+    __device__ __forceinline__ void advance(int pg) {
+        fetch(pg + PAGES);
+        id = block_of(pg + 2 * PAGES);
+    }
+};
+
 
 // A unit's query rows [R0, R0 + ROWS) as f16 tiles of 128 rows x d at `qt`,
 // by the NW warps wi = 0 .. NW - 1: CL lanes share a row (a 16-byte chunk of 8
@@ -120,6 +177,13 @@ __device__ __forceinline__ void mask_keys(float (&sv)[HK], int key0, int lq, int
     for (int j = 0; j < HK; ++j) sv[j] = j >= lo && j <= hi ? sv[j] : -INFINITY;
 }
 
+// Hands registers between the warpgroups of a CTA: every warp of a warpgroup
+// calls it.  An increase waits until the others have given up enough.
+template <int N>
+__device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // A page whose weights under a row's reference sum to more than this moves the
 // reference.  No weight of a smaller sum is above it, so all are f16.
 constexpr float kMaxSum = 256.f;
@@ -167,6 +231,10 @@ constexpr int kMmaWarp = 12;
 constexpr int kScaleWarp = 13;
 constexpr int kCopyWarp0 = 14;             // warp 14 copies K pages, warp 15 V pages
 constexpr int kThreads = 16 * 32;
+// Registers a thread: launched with kRegs, then shared out by warpgroup (0-3
+// softmax, 4-11 converters, 12-15); the shares add up to the launch's total.
+constexpr int kRegs = 128, kSoftRegs = 184, kConvRegs = 112, kAuxRegs = 104;
+static_assert(kSoftRegs + 2 * kConvRegs + kAuxRegs <= 4 * kRegs, "register shares");
 }  // namespace one
 
 template <int D>
@@ -307,6 +375,7 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
     float m = -INFINITY, l = 0.f;
     if (warp < 4) {
         // ---------------------------------------------------------- softmax
+        more_regs<kSoftRegs>();
         const float cs = row_scale[(tid & 127) % RT];
         const int pq = u.L - u.n + (rv ? r >> lg : 0);
         const int lq = (a.window > 0 && pq + 1 > a.window) ? pq + 1 - a.window : 0;
@@ -448,6 +517,7 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
         }
     } else if (warp < kMmaWarp) {
         // ---------------------------------------------------------- converters
+        fewer_regs<kConvRegs>();
         const int ct = tid - kConvWarp0 * 32, grp = ct / GT, gt = ct % GT;
         for (int st = 0; st < nst; ++st) {
             const int slot = st % STAGES;
@@ -470,7 +540,9 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
             mbar_arrive(&v_full[j]);
             mbar_arrive(&f_empty[slot]);
         }
-    } else if (warp >= kCopyWarp0) {
+    } else {
+    fewer_regs<kAuxRegs>();
+    if (warp >= kCopyWarp0) {
         // ---------------------------------------------------------- copies
         for (int st = STAGES; st < nst; ++st) {
             if (!__all_sync(0xffffffffu, wait_or_abort(&f_empty[st % STAGES], (st / STAGES + 1) & 1, a.wait_ns, abort_flag)))
@@ -531,6 +603,7 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
         // every MMA this thread issued completes before TMEM is released
         tc::commit(&done_bar);
         mbar_wait_bounded(&done_bar, 0, tcg::kWaitNs);
+    }
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -634,25 +707,26 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
 // ---------------------------------------------------------------------------
 // The two-tile kernel (d = 64 and 128, chunks of at least two tiles): 256 query
 // rows of one (sequence, kv head) per CTA, so that each stage's operand tiles
-// serve two tiles, in stages of 64 keys.
+// serve two tiles, in stages of 128 keys.
 //
-// Roles, each of which keeps a ring ahead of the next:
-//   * warps 8-11 copy and convert K, warps 12-15 V (transposed): cp.async two
-//     stages ahead into a ring of their own (a barrier of the four warps tells
+// Roles, handing over through mbarriers:
+//   * warps 8-11 copy and convert K, warps 12-15 V (transposed): cp.async a
+//     stage ahead into a ring of their own (a barrier of the four warps tells
 //     that a stage has landed and that the slot to refill has been read), block
-//     ids a stage ahead of that, then the conversion into one of two operand
-//     tiles;
-//   * one thread of warp 16 issues the MMAs.  Tile by tile: once P of stage s is
-//     in, O += P V, then S = Q K^T of stage s + 2 into the buffer that held P(s)
-//     (the MMAs of one thread run in issue order).  S has two buffers per tile,
-//     so a tile's next scores are there when its softmax is done;
+//     ids a stage ahead of that, then the conversion into the K tile or into one
+//     of two V^T tiles;
+//   * one thread of warp 16 issues the MMAs, tile by tile in turn: once P of
+//     stage s is in, O += P V, then S = Q K^T of stage s + 1 over the same
+//     columns (the MMAs of one thread run in issue order);
 //   * warp 17 prepares the page scales, a stage ahead;
 //   * warps 0-3 and 4-7 (a warpgroup per tile, thread = row = TMEM lane) weigh
-//     the stage as the one-tile kernel does -- under the reference the row has,
-//     one read of S, P over the S just read -- and read the next stage's scores
-//     before they hand P over.
-// A 64-key stage halves what a row holds in registers against 128 keys, which is
-// what lets it be read once; the tensor cores lose little (N = 64 for S).
+//     the stage in two halves of 64 keys as the one-tile kernel does -- under
+//     the reference the row has, one read of S, P over S already read.
+// The two tiles ping-pong: while one tile's warps weigh, the tensor cores run
+// the other's MMAs.  Stages of 64 keys with two S buffers a tile measured 1819
+// against 1464 us (8 x 20K, chunks of 512 tokens): at N = 64 the score MMAs
+// read Q from shared memory twice as often for the same work, and the second
+// buffer did not make up for it.
 namespace two {
 constexpr int kTiles = 2;
 constexpr int kKWarp0 = 8, kVWarp0 = 12;   // warps 8-11 convert K, 12-15 V
@@ -661,39 +735,37 @@ constexpr int kThreads = 20 * 32;          // (warps 18 and 19 fill the last war
 // Registers a thread: launched with kRegs, then shared out by warpgroup -- the
 // softmax holds 64 scores.  The shares add up to the launch's total, or less,
 // so that every increase is granted.
-constexpr int kRegs = 96, kSoftRegs = 112, kConvRegs = 96, kAuxRegs = 64;
+constexpr int kRegs = 96, kSoftRegs = 136, kConvRegs = 72, kAuxRegs = 64;
 static_assert(2 * kSoftRegs + 2 * kConvRegs + kAuxRegs <= 5 * kRegs, "register shares");
 constexpr int kBar = 2;                    // named barriers of the converter groups: 2 (K), 3 (V)
-constexpr int kStg = 3;                    // stages in a staging ring
+constexpr int kStg = 2;                    // stages in a staging ring
 }  // namespace two
 
 template <int D>
 struct TwoGeo {
-    static constexpr int KEYS = tcg::kKeys, PAGES = KEYS / kBS;
+    static constexpr int KEYS = 128, PAGES = KEYS / kBS, GRAN = KEYS / tcg::kKeys;
     static constexpr int QTB = D / 64 * 128 * 128;      // one Q tile: 128 rows x d
-    static constexpr int KTB = D / 64 * KEYS * 128;     // a K tile: 64 keys x d
-    static constexpr int VTB = D * 128;                 // a V^T tile: d rows x 64 keys
-    static constexpr int SLOT = KEYS * D;               // one staging slot: 64 fp8 rows
-    static constexpr int QT = 0, KT = QT + two::kTiles * QTB, VT = KT + 2 * KTB, STG = VT + 2 * VTB;
-    static constexpr int SMEM = STG + 2 * two::kStg * SLOT;   // 176 KB at d = 128, 88 KB at 64
-    // TMEM columns per tile: two S buffers (P over the first half of each), then O
-    static constexpr uint32_t OC = 2 * KEYS, TC = 256, COLS = two::kTiles * TC;
+    static constexpr int KAT = KEYS * 128;              // one 128-byte atom column of the K tile
+    static constexpr int KTB = D / 64 * KAT;            // the K tile: 128 keys x d
+    static constexpr int VAT = D * 128;                 // one atom column of a V^T tile: d rows x 64 keys
+    static constexpr int VTB = GRAN * VAT;              // a V^T tile: d rows x 128 keys
+    static constexpr int GSLOT = tcg::kKeys * D;        // 64 staged fp8 rows
+    static constexpr int SLOT = GRAN * GSLOT;           // one staging slot
+    static constexpr int QT = 0, KT = QT + two::kTiles * QTB, VT = KT + KTB, STG = VT + 2 * VTB;
+    static constexpr int SMEM = STG + 2 * two::kStg * SLOT;   // 224 KB at d = 128, 112 KB at 64
+    // TMEM columns per tile: S (P over its first half), then O
+    static constexpr uint32_t OC = KEYS, TC = 256, COLS = two::kTiles * TC;
     static_assert(OC + D <= TC, "TMEM columns");
 };
-
-template <int N>
-__device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 template <int D>
 __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(const Args a) {
     using namespace two;
     using Tg = TwoGeo<D>;
-    constexpr int KEYS = Tg::KEYS, PAGES = Tg::PAGES;
+    constexpr int KEYS = Tg::KEYS, PAGES = Tg::PAGES, HK = KEYS / 2;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], c_full[2], c_empty[2];
-    __shared__ uint64_t s_full[kTiles][2], p_full[kTiles][2], done_bar;
+    __shared__ uint64_t k_full, k_empty, v_full[2], v_empty[2], c_full[2], c_empty[2];
+    __shared__ uint64_t s_full[kTiles], p_full[kTiles], done_bar;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_sh;
     __shared__ float4 psc[2][PAGES];
@@ -703,17 +775,17 @@ __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(con
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
+        mbar_init(&k_full, 128);
+        mbar_init(&k_empty, 1);            // tcgen05.commit
         for (int j = 0; j < 2; ++j) {
-            mbar_init(&k_full[j], 128);
-            mbar_init(&k_empty[j], 1);     // tcgen05.commit
             mbar_init(&v_full[j], 128);
             mbar_init(&v_empty[j], 1);
             mbar_init(&c_full[j], 1);      // the scale warp
             mbar_init(&c_empty[j], 8);     // the softmax warps
-            for (int i = 0; i < kTiles; ++i) {
-                mbar_init(&s_full[i][j], 1);
-                mbar_init(&p_full[i][j], 128);
-            }
+        }
+        for (int i = 0; i < kTiles; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 128);
         }
         mbar_init(&done_bar, 1);
         abort_sh = 0;
@@ -759,8 +831,8 @@ __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(con
             const int i = ct + it * 128, p = i / CPP, ci = i % CPP;   // p is the same for a warp
             const int id = __shfl_sync(0xffffffffu, ids, p);
             if (p < np) {
-                const int k = p * kBS + ci / CPR, c = ci % CPR;
-                cp_async16(dst + (is_v ? stg_v<D>(k, c) : stg_k<D>(k, c)),
+                const int k = (p % 4) * kBS + ci / CPR, c = ci % CPR;
+                cp_async16(dst + (p / 4) * Tg::GSLOT + (is_v ? stg_v<D>(k, c) : stg_k<D>(k, c)),
                            cache + (static_cast<int64_t>(id) * a.num_kv_heads + hk) * (kBS * D) + ci * 16);
             }
         }
@@ -768,10 +840,9 @@ __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(con
     };
     int next_ids = 0;
     if (warp >= kKWarp0 && warp < kMmaWarp) {
-        const int id0 = blocks_of(0), id1 = blocks_of(1);
-        next_ids = blocks_of(2);
+        const int id0 = blocks_of(0);
+        next_ids = blocks_of(1);
         copy_stage(0, id0);
-        copy_stage(1, id1);
     }
     if (warp < kMmaWarp)
         build_q_tiles<D, kTiles * 128, 1, kMmaWarp>(a, u, hk, u.R0, sm + Tg::QT, row_scale, warp, lane);
@@ -808,123 +879,151 @@ __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(con
             for (int c = 0; c < D / 32; ++c) tc::st32(trow + Tg::OC + 32 * c, z);
             tc::wait_st();
         }
-        // (the waits' results are made warp-uniform: the TMEM loads are collective)
-        auto wait_s = [&](int s) {
-            return __all_sync(0xffffffffu, wait_or_abort(&s_full[ti][s & 1], (s >> 1) & 1, a.wait_ns, abort_flag));
-        };
-        float sv[KEYS];
-        auto load = [&](int s) {                  // the row's scores of stage s, masked
-            const uint32_t scol = trow + (s & 1) * KEYS;
-            tc::fence_after_sync();
-            tc::ld32(scol, *reinterpret_cast<float(*)[32]>(sv));
-            tc::ld32(scol + 32, *reinterpret_cast<float(*)[32]>(sv + 32));
+        float sv[HK];
+        auto load = [&](int s, int hf) {          // half hf of the row's scores of stage s, masked
+            tc::ld32(trow + HK * hf, *reinterpret_cast<float(*)[32]>(sv));
+            tc::ld32(trow + HK * hf + 32, *reinterpret_cast<float(*)[32]>(sv + 32));
             tc::wait_ld(*reinterpret_cast<float(*)[32]>(sv));
             tc::wait_ld(*reinterpret_cast<float(*)[32]>(sv + 32));
             const int t0 = (sp0 + s * PAGES) * kBS;
             if (!(t0 + KEYS <= sp1 * kBS && t0 + KEYS - 1 <= wpos0 && t0 >= wlo1))
-                mask_keys<KEYS>(sv, t0, lq, pq, sp1 * kBS);
+                mask_keys<HK>(sv, t0 + HK * hf, lq, pq, sp1 * kBS);
         };
-        bool ok = nst == 0 || wait_s(0);
-        if (ok && nst > 0 && warp_rows) load(0);
-        for (int st = 0; st < nst && ok; ++st) {
-            const int buf = st & 1;
-            if (!__all_sync(0xffffffffu, wait_or_abort(&c_full[buf], (st >> 1) & 1, a.wait_ns, abort_flag))) break;
+        for (int st = 0; st < nst; ++st) {
+            // S of stage st is in; its commit also covers the P V of stage
+            // st - 1, so O is complete and P's columns are free.  (The waits'
+            // result is made warp-uniform: the TMEM loads are collective.)
+            if (!__all_sync(0xffffffffu, wait_or_abort(&s_full[ti], st & 1, a.wait_ns, abort_flag) &&
+                                             wait_or_abort(&c_full[st & 1], (st >> 1) & 1, a.wait_ns, abort_flag)))
+                break;
             if (warp_rows) {
+                tc::fence_after_sync();
                 const int t0 = (sp0 + st * PAGES) * kBS;
-                const float4* scale = psc[buf];
-                float ls, top = 0.f;
-                // as in the one-tile kernel: under the reference the row has, or
-                // the long way for its first keys and for a page that outgrows it
-                bool look = __any_sync(0xffffffffu, m == -INFINITY && pq >= t0 && lq < min(t0 + KEYS, sp1 * kBS));
+                float lst = 0.f;
 #pragma unroll 1
-                while (true) {
-                    if (look) {
-                        float mx = -INFINITY;
-#pragma unroll
-                        for (int pg = 0; pg < PAGES; ++pg) {
-                            float big = -INFINITY;
-#pragma unroll
-                            for (int i = 0; i < kBS; ++i) big = fmaxf(big, sv[kBS * pg + i]);
-                            const float4 w = scale[pg];
-                            mx = fmaxf(mx, fmaf(big, cs * w.x, w.y));
-                        }
-                        const float mn = fmaxf(m, mx);
-                        const bool upd = mn > m && (m == -INFINITY || top > kMaxSum);
-                        const bool held = upd && m != -INFINITY;
-                        float alpha = 1.f;
-                        if (upd) {
-                            alpha = fast_exp2(m - mn);
-                            l *= alpha;
-                            m = mn;
-                        }
-                        if (__any_sync(0xffffffffu, held)) {
-                            // O = O * alpha for the warp's rows, once the value MMAs of stage st - 1 are in
-                            ok = __all_sync(0xffffffffu, wait_or_abort(&v_empty[buf ^ 1], ((st - 1) >> 1) & 1, a.wait_ns,
-                                                                       abort_flag));
-                            if (!ok) break;
-                            tc::fence_after_sync();
+                for (int hf = 0; hf < 2; ++hf) {
+                    load(st, hf);
+                    const float4* scale = psc[st & 1] + PAGES / 2 * hf;
+                    float ls, top = 0.f;
+                    // as in the one-tile kernel: under the reference the row has,
+                    // or the long way for its first keys (looked for in the whole
+                    // stage, at its first half) and for a page that outgrows it
+                    bool look = hf == 0 && __any_sync(0xffffffffu, m == -INFINITY && pq >= t0 &&
+                                                                       lq < min(t0 + KEYS, sp1 * kBS));
 #pragma unroll 1
-                            for (int c = 0; c < D / 16; ++c) {   // (16 at a time: the scores are in registers)
-                                float x[16];
-                                tc::ld16(trow + Tg::OC + 16 * c, x);
-                                tc::wait_ld(x);
+                    while (true) {
+                        if (look) {
+                            float mx = -INFINITY;
+                            auto page_max = [&](const float* x, const float4& w) {
+                                float big = -INFINITY;
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) x[j] *= alpha;
-                                tc::st16(trow + Tg::OC + 16 * c, x);
+                                for (int i = 0; i < kBS; ++i) big = fmaxf(big, x[i]);
+                                mx = fmaxf(mx, fmaf(big, cs * w.x, w.y));
+                            };
+#pragma unroll
+                            for (int pg = 0; pg < PAGES / 2; ++pg) page_max(sv + kBS * pg, scale[pg]);
+                            if (hf == 0) {
+#pragma unroll 1
+                                for (int pg = PAGES / 2; pg < PAGES; ++pg) {
+                                    float x[16];
+                                    tc::ld16(trow + kBS * pg, x);
+                                    tc::wait_ld(x);
+                                    mask_keys<16>(x, t0 + kBS * pg, lq, pq, sp1 * kBS);
+                                    page_max(x, scale[pg]);
+                                }
+                            }
+                            const float mn = fmaxf(m, mx);
+                            const bool upd = mn > m && (m == -INFINITY || top > kMaxSum);
+                            const bool held = upd && m != -INFINITY;
+                            float alpha = 1.f;
+                            if (upd) {
+                                alpha = fast_exp2(m - mn);
+                                l *= alpha;
+                                lst *= alpha;
+                                m = mn;
+                            }
+                            if (__any_sync(0xffffffffu, held)) {
+                                // O = O * alpha for the warp's rows (16 columns at a time: the scores are in registers)
+#pragma unroll 1
+                                for (int c = 0; c < D / 16; ++c) {
+                                    float x[16];
+                                    tc::ld16(trow + Tg::OC + 16 * c, x);
+                                    tc::wait_ld(x);
+#pragma unroll
+                                    for (int j = 0; j < 16; ++j) x[j] *= alpha;
+                                    tc::st16(trow + Tg::OC + 16 * c, x);
+                                }
+                                // ... and for the second half the first half's
+                                // weights, which are f16 already: one more
+                                // rounding of 2^-11, where a reference moves
+                                // within a stage
+                                if (hf == 1) {
+                                    tc::wait_st();
+#pragma unroll 1
+                                    for (int c = 0; c < HK / 32; ++c) {
+                                        float x[16];
+                                        tc::ld16(trow + 16 * c, x);
+                                        tc::wait_ld(x);
+#pragma unroll
+                                        for (int j = 0; j < 16; ++j) {
+                                            const uint32_t y = __float_as_uint(x[j]);
+                                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y));
+                                            x[j] = __uint_as_float(pack_f16x2(f.x * alpha, f.y * alpha));
+                                        }
+                                        tc::st16(trow + 16 * c, x);
+                                    }
+                                }
                             }
                         }
+                        ls = top = 0.f;
+                        weigh_keys<HK>(sv, scale, cs, m, trow + HK / 2 * hf, ls, top);
+                        if (look) break;
+                        look = __any_sync(0xffffffffu, top > kMaxSum);
+                        if (!look) break;
                     }
-                    ls = top = 0.f;
-                    weigh_keys<KEYS>(sv, scale, cs, m, trow + buf * KEYS, ls, top);
-                    if (look) break;
-                    look = __any_sync(0xffffffffu, top > kMaxSum);
-                    if (!look) break;
+                    lst += ls;
                 }
-                if (!ok) break;
-                l += ls;
+                l += lst;
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&c_empty[buf]);
-            if (st + 1 < nst) {
-                // the next stage's scores move to registers before P is handed
-                // over: a load would wait for the value MMAs, which then run
-                ok = wait_s(st + 1);
-                if (!ok) break;
-                if (warp_rows) load(st + 1);
-            }
+            if (lane == 0) mbar_arrive(&c_empty[st & 1]);
             if (warp_rows) {
                 tc::wait_st();
                 tc::fence_before_sync();
             }
-            mbar_arrive(&p_full[ti][buf]);     // P (and the rescaled O) are in TMEM
+            mbar_arrive(&p_full[ti]);      // P (and the rescaled O) are in TMEM
         }
     } else if (warp < kMmaWarp) {
         // ---------------------------------------------------------- converters of K or of V
         fewer_regs<kConvRegs>();
         const int bar = kBar + (is_v ? 1 : 0);
-        uint64_t* full = is_v ? v_full : k_full;
-        uint64_t* empty = is_v ? v_empty : k_empty;
+        const uint8_t* ring = sm + Tg::STG + (is_v ? kStg * Tg::SLOT : 0);
         bool ok = true;
         for (int st = 0; st < nst; ++st) {
-            cp_async_wait<1>();                // this thread's copies of stage st have landed
+            cp_async_wait<0>();                // this thread's copies of stage st have landed
             // everyone's have; the slot of stage st - 1 has been read (or all give up)
             if (named_bar_or(bar, 128, !ok)) break;
-            copy_stage(st + 2, next_ids);
-            next_ids = blocks_of(st + 3);
+            copy_stage(st + 1, next_ids);
+            next_ids = blocks_of(st + 2);
             const int j = st & 1;
-            // tile j is free once the MMAs of stage st - 2 that read it have completed
-            ok = st < 2 || wait_or_abort(&empty[j], ((st >> 1) + 1) & 1, a.wait_ns, abort_flag);
+            // the K tile is free once the score MMAs of stage st - 1 have completed,
+            // V^T tile j once the value MMAs of stage st - 2 have
+            if (is_v) ok = st < 2 || wait_or_abort(&v_empty[j], ((st >> 1) + 1) & 1, a.wait_ns, abort_flag);
+            else ok = st < 1 || wait_or_abort(&k_empty, (st - 1) & 1, a.wait_ns, abort_flag);
             if (!ok) continue;                 // (to the barrier, where the group leaves together)
             const int pg = sp0 + st * PAGES;
-            if (is_v) {
-                // (the conversion's V rows follow 64 K rows in its source)
-                convert_stage_v<D>(sm + Tg::STG + (kStg + st % kStg) * Tg::SLOT - tcg::kKeys * D,
-                                   sm + Tg::VT + j * Tg::VTB, ct, pg * kBS, min(PAGES, sp1 - pg), kmin, kmax);
-            } else {
-                convert_stage_k<D>(sm + Tg::STG + st % kStg * Tg::SLOT, sm + Tg::KT + j * Tg::KTB, ct);
+            const uint8_t* slot = ring + st % kStg * Tg::SLOT;
+#pragma unroll 1
+            for (int g = 0; g < Tg::GRAN; ++g) {
+                const int np = sp1 - pg - g * (tcg::kKeys / kBS);    // pages left
+                if (is_v)   // (the conversion's V rows follow 64 K rows in its source)
+                    convert_stage_v<D>(slot + g * Tg::GSLOT - tcg::kKeys * D, sm + Tg::VT + j * Tg::VTB + g * Tg::VAT, ct,
+                                       (pg + g * (tcg::kKeys / kBS)) * kBS, min(tcg::kKeys / kBS, np), kmin, kmax);
+                else if (np > 0)   // an empty granule's keys are masked
+                    convert_stage_k<D, Tg::KAT>(slot + g * Tg::GSLOT, sm + Tg::KT + g * (tcg::kKeys * 128), ct);
             }
             tc::fence_proxy_async_smem();      // the tile is read by the tensor cores
-            mbar_arrive(&full[j]);
+            mbar_arrive(is_v ? &v_full[j] : &k_full);
         }
         cp_async_wait<0>();                    // no copy lands after the CTA is gone
     } else {
@@ -946,45 +1045,43 @@ __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(con
         constexpr uint32_t id_s = tc::idesc_f16_f32(128, KEYS);
         constexpr uint32_t id_o = tc::idesc_f16_f32(128, D);
         const bool stall_cta = blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0;
-        const uint64_t qd0 = tc::desc_k_sw128(sb + Tg::QT), kd0 = tc::desc_k_sw128(sb + Tg::KT),
+        const uint64_t qd0 = tc::desc_k_sw128(sb + Tg::QT), kd = tc::desc_k_sw128(sb + Tg::KT),
                        vd0 = tc::desc_k_sw128(sb + Tg::VT);
-        // S = Q K^T of stage s for tile i into the stage's buffer
+        // S = Q K^T of stage s for tile i
         auto issue_s = [&](int i, int s) {
             if (i == 0) {
-                if (!wait_or_abort(&k_full[s & 1], (s >> 1) & 1, a.wait_ns, abort_flag)) return false;
+                if (!wait_or_abort(&k_full, s & 1, a.wait_ns, abort_flag)) return false;
                 tc::fence_after_sync();
             }
-            const uint32_t sc = tm + i * Tg::TC + (s & 1) * KEYS;
-            const uint64_t qd = tc::desc_at(qd0, i * Tg::QTB), kd = tc::desc_at(kd0, (s & 1) * Tg::KTB);
+            const uint64_t qd = tc::desc_at(qd0, i * Tg::QTB);
             if (!(s == a.stall_stage && stall_cta)) {   // test hook: this stage's S never arrives
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
-                    tc::mma_f16(sc, tc::desc_at(qd, (ks >> 2) * 16384 + (ks & 3) * 32),
-                                tc::desc_at(kd, (ks >> 2) * (KEYS * 128) + (ks & 3) * 32), id_s, ks > 0);
-                tc::commit(&s_full[i][s & 1]);
+                    tc::mma_f16(tm + i * Tg::TC, tc::desc_at(qd, (ks >> 2) * 16384 + (ks & 3) * 32),
+                                tc::desc_at(kd, (ks >> 2) * Tg::KAT + (ks & 3) * 32), id_s, ks > 0);
+                tc::commit(&s_full[i]);
             }
-            if (i == kTiles - 1) tc::commit(&k_empty[s & 1]);   // the K tile is free when the score MMAs complete
+            if (i == kTiles - 1) tc::commit(&k_empty);   // the K tile is free when the score MMAs complete
             return true;
         };
         bool ok = true;
-        for (int s = 0; s < 2 && s < nst && ok; ++s)
-            for (int i = 0; i < kTiles && ok; ++i) ok = issue_s(i, s);
+        for (int i = 0; i < kTiles && ok && nst > 0; ++i) ok = issue_s(i, 0);
         for (int st = 0; st < nst && ok; ++st)
             for (int i = 0; i < kTiles && ok; ++i) {
-                const int buf = st & 1;
-                ok = wait_or_abort(&p_full[i][buf], (st >> 1) & 1, a.wait_ns, abort_flag) &&
-                     (i > 0 || wait_or_abort(&v_full[buf], (st >> 1) & 1, a.wait_ns, abort_flag));
+                const int j = st & 1;
+                ok = wait_or_abort(&p_full[i], st & 1, a.wait_ns, abort_flag) &&
+                     (i > 0 || wait_or_abort(&v_full[j], (st >> 1) & 1, a.wait_ns, abort_flag));
                 if (!ok) break;
                 tc::fence_after_sync();
-                // O += P V: P (128 rows x 64 keys) from the first half of the stage's S columns
-                const uint32_t oc = tm + i * Tg::TC + Tg::OC;
-                const uint64_t vd = tc::desc_at(vd0, buf * Tg::VTB);
+                // O += P V: P (128 rows x 128 keys) from the first half of the S columns
+                const uint32_t pc = tm + i * Tg::TC;
+                const uint64_t vd = tc::desc_at(vd0, j * Tg::VTB);
 #pragma unroll
                 for (int ks = 0; ks < KEYS / 16; ++ks)
-                    tc::mma_f16_ts(oc, oc - Tg::OC + buf * KEYS + ks * 8, tc::desc_at(vd, ks * 32), id_o, 1);
-                // the V^T tile is free, and both O complete, when both tiles' value MMAs complete
-                if (i == kTiles - 1) tc::commit(&v_empty[buf]);
-                if (st + 2 < nst) ok = issue_s(i, st + 2);
+                    tc::mma_f16_ts(pc + Tg::OC, pc + ks * 8, tc::desc_at(vd, (ks >> 2) * Tg::VAT + (ks & 3) * 32), id_o, 1);
+                // the V^T tile is free when both tiles' value MMAs complete
+                if (i == kTiles - 1) tc::commit(&v_empty[j]);
+                if (st + 1 < nst) ok = issue_s(i, st + 1);
             }
         // every MMA this thread issued completes before TMEM is released
         tc::commit(&done_bar);
@@ -1063,9 +1160,18 @@ static cudaError_t launch_with(void (*kernel)(const Args), std::atomic<uint64_t>
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+// Whether a kernel is launched with the registers that its warpgroups' shares
+// add up to: with fewer an increase would never be granted.
+static bool launched_with(void (*kernel)(const Args), int regs) {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, kernel) == cudaSuccess && at.numRegs >= regs;
+}
+
 template <int D, int REP>
 static cudaError_t launch_one_rep(const Args& a, dim3 grid, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
+    static const bool regs_ok = launched_with(paged_prefill_one_kernel<D, REP>, one::kRegs);
+    if (!regs_ok) return cudaErrorInvalidConfiguration;
     return launch_with(paged_prefill_one_kernel<D, REP>, done, OneGeo<D>::SMEM + 1024, grid, one::kThreads, a, s);
 }
 
@@ -1090,11 +1196,7 @@ static cudaError_t launch_block_g(int kind, const Args& a, int batch, cudaStream
     } else {
         if constexpr (D < 256) {
             static std::atomic<uint64_t> done{0};
-            // the register shares rest on the launch's total
-            static const bool regs_ok = [] {
-                cudaFuncAttributes at;
-                return cudaFuncGetAttributes(&at, paged_prefill_two_kernel<D>) == cudaSuccess && at.numRegs >= two::kRegs;
-            }();
+            static const bool regs_ok = launched_with(paged_prefill_two_kernel<D>, two::kRegs);
             if (!regs_ok) return cudaErrorInvalidConfiguration;
             const int pairs = (a.tiles + two::kTiles - 1) / two::kTiles;
             e = launch_with(paged_prefill_two_kernel<D>, done, static_cast<size_t>(TwoGeo<D>::SMEM) + 1024,
