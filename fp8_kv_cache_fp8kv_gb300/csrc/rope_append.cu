@@ -56,7 +56,6 @@ struct Rope {
     const uint8_t* freq_axis;   // [rotary_dim / 2], or null: axis 0
     int axes;
     int rot;                    // items of a row that turn: rotary_dim / 16
-    int pairs;                  // 0: pairs (i, i + R/2); 1: pairs (2i, 2i + 1)
 };
 
 struct Rows {
@@ -128,8 +127,9 @@ __device__ __forceinline__ void fill_table(float4* tab, const Rope& rp, int64_t 
 
 // First elements of the two 8-element halves of item j of a row: a turning
 // item holds both elements of each of its 8 pairs.
+template <bool PAIRS>
 __device__ __forceinline__ void item_place(const Rope& rp, int j, int& e0, int& e1) {
-    if (j < rp.rot && !rp.pairs) {
+    if (!PAIRS && j < rp.rot) {
         e0 = 8 * j;
         e1 = 8 * (rp.rot + j);
     } else {
@@ -148,6 +148,7 @@ __device__ __forceinline__ void unpack(const uint4& a, const uint4& b, float (&x
 }
 
 // Turns item j (j < rot) of a row of token `tok` of the table.
+template <bool PAIRS>
 __device__ __forceinline__ void turn(float (&x)[16], const float4* tab, const Rope& rp, int tok, int j) {
     const float4* e = tab + tok * 4 * rp.rot + j;
 #pragma unroll
@@ -158,40 +159,77 @@ __device__ __forceinline__ void turn(float (&x)[16], const float4* tab, const Ro
             const float c = h ? cs.z : cs.x, s = h ? cs.w : cs.y;
             const int i = 2 * k + h;
             // the pair of frequency 8j + i: elements i and 8 + i of the item, or 2i and 2i + 1
-            const float a = rp.pairs ? x[2 * i] : x[i], b = rp.pairs ? x[2 * i + 1] : x[8 + i];
+            float& a = PAIRS ? x[2 * i] : x[i];
+            float& b = PAIRS ? x[2 * i + 1] : x[8 + i];
             const float u = fmaf(a, c, -(b * s)), v = fmaf(b, c, a * s);
-            if (rp.pairs) {
-                x[2 * i] = u;
-                x[2 * i + 1] = v;
-            } else {
-                x[i] = u;
-                x[8 + i] = v;
-            }
+            a = u;
+            b = v;
         }
     }
 }
 
-// One q row item: read, turn, round once to bf16, write.  A thread reads its
-// item before it writes it and no other thread touches it, so q_out may be q.
-template <int D>
-__device__ __forceinline__ void q_item(const Rows& rw, const Rope& rp, const float4* tab, int64_t t0, int tok, int h,
-                                       int j) {
-    int e0, e1;
-    item_place(rp, j, e0, e1);
-    const uint16_t* src = rw.q + (t0 + tok) * rw.q_stride + static_cast<int64_t>(h) * D;
-    uint16_t* dst = rw.q_out + ((t0 + tok) * rw.hq + h) * D;
-    uint4 a = *reinterpret_cast<const uint4*>(src + e0), b = *reinterpret_cast<const uint4*>(src + e1);
-    if (j < rp.rot) {
-        float x[16];
-        unpack(a, b, x);
-        turn(x, tab, rp, tok, j);
-        a = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                       pack_bf16x2(x[6], x[7]));
-        b = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]),
-                       pack_bf16x2(x[14], x[15]));
+__device__ __forceinline__ void pack(const float (&x)[16], uint4& a, uint4& b) {
+    a = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    b = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]),
+                   pack_bf16x2(x[14], x[15]));
+}
+
+// Item i of `heads` rows a token -> (token, row, item of the row).  The
+// quotient by `heads` through a reciprocal: i / IPR < 2^20 and heads < 2^16,
+// so (row + 1/2) / heads stays 2^-17 away from a whole number, and two
+// roundings of a number below 16 move it by 2^-19.
+template <int IPR>
+__device__ __forceinline__ void item_of(int i, int heads, float inv, int& tok, int& r, int& j) {
+    const int row = i / IPR;
+    tok = static_cast<int>((static_cast<float>(row) + 0.5f) * inv);
+    r = row - tok * heads;
+    j = i % IPR;
+}
+
+// The q rows of heads [h0, h1) of `cnt` tokens from t0: read, turn, round once
+// to bf16, write; two items of a thread in flight.  A thread reads its items
+// before it writes them and no other thread touches them, so q_out may be q.
+// The first two are read before the rotation table is waited for (`ready`).
+template <int D, bool PAIRS, typename F>
+__device__ __forceinline__ void q_rows(const Rows& rw, const Rope& rp, const float4* tab, int64_t t0, int cnt, int h0,
+                                       int h1, int tid, F ready) {
+    constexpr int IPR = D / 16;
+    const int heads = h1 - h0, n = cnt * heads * IPR;
+    const float inv = 1.f / static_cast<float>(heads);
+    bool waited = false;
+    for (int i0 = tid; i0 < n || !waited; i0 += 2 * kThreads) {
+        uint4 a[2], b[2];
+        int tok[2], e0[2], e1[2], j[2], h[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int i = i0 + u * kThreads;
+            if (i < n) {
+                item_of<IPR>(i, heads, inv, tok[u], h[u], j[u]);
+                item_place<PAIRS>(rp, j[u], e0[u], e1[u]);
+                const uint16_t* src = rw.q + (t0 + tok[u]) * rw.q_stride + static_cast<int64_t>(h0 + h[u]) * D;
+                a[u] = *reinterpret_cast<const uint4*>(src + e0[u]);
+                b[u] = *reinterpret_cast<const uint4*>(src + e1[u]);
+            }
+        }
+        if (!waited) {
+            ready();
+            waited = true;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if (i0 + u * kThreads < n) {
+                if (j[u] < rp.rot) {
+                    float x[16];
+                    unpack(a[u], b[u], x);
+                    turn<PAIRS>(x, tab, rp, tok[u], j[u]);
+                    pack(x, a[u], b[u]);
+                }
+                uint16_t* dst = rw.q_out + ((t0 + tok[u]) * rw.hq + h0 + h[u]) * D;
+                *reinterpret_cast<uint4*>(dst + e0[u]) = a[u];
+                *reinterpret_cast<uint4*>(dst + e1[u]) = b[u];
+            }
+        }
     }
-    *reinterpret_cast<uint4*>(dst + e0) = a;
-    *reinterpret_cast<uint4*>(dst + e1) = b;
 }
 
 // 16 values divided by the scale (one IEEE division each) as FP8 codes.
@@ -238,70 +276,70 @@ struct SlotArgs {
 };
 
 // FMT: fp8kv_cache_format.  grid: (blocks of kTok tokens, head splits); split
-// y takes an equal run of the rows of a token (q heads, then k heads, then v
-// heads).
-template <int D, int FMT>
+// y takes an equal run of the q heads and an equal run of the kv heads.
+template <int D, int FMT, bool PAIRS>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const SlotArgs a) {
     constexpr int IPR = D / 16;   // items per row
     extern __shared__ float4 tab[];
+    __shared__ int64_t slot_sh[kTok];
     griddep_launch_dependents();
     griddep_wait();               // the inputs and the cache may be the previous grid's
     const Rows& rw = a.rw;
     const int tid = threadIdx.x;
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTok;
     const int cnt = static_cast<int>(rw.num_tokens - t0 < kTok ? rw.num_tokens - t0 : kTok);
-    fill_table(tab, a.rp, t0, cnt, 0, rw.num_tokens, tid);
-    __shared__ int64_t slot_sh[kTok];
-    if (tid < cnt) {
-        const int64_t s = __ldg(a.slots + t0 + tid);
-        slot_sh[tid] = s < a.num_slots ? s : -1;
-    }
-    __syncthreads();
-    const int hq = rw.q ? rw.hq : 0;
-    const int64_t rows = hq + 2 * static_cast<int64_t>(rw.hkv);
-    const int r0 = static_cast<int>(rows * blockIdx.y / gridDim.y), r1 = static_cast<int>(rows * (blockIdx.y + 1) / gridDim.y);
-    const int per_tok = (r1 - r0) * IPR;
-#pragma unroll 2
-    for (int i = tid; i < cnt * per_tok; i += kThreads) {
-        const int tok = i / per_tok, rem = i - tok * per_tok;
-        const int r = r0 + rem / IPR, j = rem % IPR;
-        if (r < hq) {
-            q_item<D>(rw, a.rp, tab, t0, tok, r, j);
-            continue;
+    auto ready = [&]() {          // the rotation table and the slots
+        fill_table(tab, a.rp, t0, cnt, 0, rw.num_tokens, tid);
+        if (tid < cnt) {
+            const int64_t s = __ldg(a.slots + t0 + tid);
+            slot_sh[tid] = s < a.num_slots ? s : -1;
         }
+        __syncthreads();
+    };
+    const int64_t y = blockIdx.y, ny = gridDim.y;
+    if (rw.q)
+        q_rows<D, PAIRS>(rw, a.rp, tab, t0, cnt, static_cast<int>(rw.hq * y / ny), static_cast<int>(rw.hq * (y + 1) / ny),
+                         tid, ready);
+    else
+        ready();
+    const int kv0 = static_cast<int>(rw.hkv * y / ny), kv1 = static_cast<int>(rw.hkv * (y + 1) / ny);
+    const int heads = kv1 - kv0;
+    const float inv = 1.f / static_cast<float>(heads);
+    for (int i = tid; i < cnt * heads * IPR; i += kThreads) {
+        int tok, h, j;
+        item_of<IPR>(i, heads, inv, tok, h, j);
+        h += kv0;
         const int64_t slot = slot_sh[tok];
         if (slot < 0) continue;
-        const bool is_v = r >= hq + rw.hkv;
-        const int h = r - hq - (is_v ? rw.hkv : 0);
-        int e0 = 16 * j, e1 = 16 * j + 8;
-        if (!is_v) item_place(a.rp, j, e0, e1);
-        const uint16_t* src = (is_v ? rw.v + (t0 + tok) * rw.v_stride : rw.k + (t0 + tok) * rw.k_stride) +
-                              static_cast<int64_t>(h) * D;
-        const uint4 x0 = __ldcs(reinterpret_cast<const uint4*>(src + e0));
-        const uint4 x1 = __ldcs(reinterpret_cast<const uint4*>(src + e1));
-        float x[16];
-        unpack(x0, x1, x);
-        const bool turns = !is_v && j < a.rp.rot;
-        if (turns) turn(x, tab, a.rp, tok, j);
+        int e0, e1;
+        item_place<PAIRS>(a.rp, j, e0, e1);
+        const uint16_t* ks = rw.k + (t0 + tok) * rw.k_stride + static_cast<int64_t>(h) * D;
+        const uint16_t* vs = rw.v + (t0 + tok) * rw.v_stride + static_cast<int64_t>(h) * D + 16 * j;
+        uint4 k0 = __ldcs(reinterpret_cast<const uint4*>(ks + e0));
+        uint4 k1 = __ldcs(reinterpret_cast<const uint4*>(ks + e1));
+        const uint4 v0 = __ldcs(reinterpret_cast<const uint4*>(vs));
+        const uint4 v1 = __ldcs(reinterpret_cast<const uint4*>(vs + 8));
         const int64_t blk = slot / a.block_size, off = slot - blk * a.block_size;
         const int64_t row = ((blk * rw.hkv + h) * a.block_size + off) * D;
+        float x[16];
+        unpack(k0, k1, x);
+        if (j < a.rp.rot) turn<PAIRS>(x, tab, a.rp, tok, j);
         if constexpr (FMT == FP8KV_CACHE_BF16) {
-            uint16_t* dst = static_cast<uint16_t*>(is_v ? a.v_cache : a.k_cache) + row;
-            uint4 y0 = x0, y1 = x1;
-            if (turns) {
-                y0 = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                pack_bf16x2(x[6], x[7]));
-                y1 = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]),
-                                pack_bf16x2(x[14], x[15]));
-            }
-            *reinterpret_cast<uint4*>(dst + e0) = y0;
-            *reinterpret_cast<uint4*>(dst + e1) = y1;
+            uint16_t* kd = static_cast<uint16_t*>(a.k_cache) + row;
+            uint16_t* vd = static_cast<uint16_t*>(a.v_cache) + row + 16 * j;
+            if (j < a.rp.rot) pack(x, k0, k1);
+            *reinterpret_cast<uint4*>(kd + e0) = k0;
+            *reinterpret_cast<uint4*>(kd + e1) = k1;
+            *reinterpret_cast<uint4*>(vd) = v0;
+            *reinterpret_cast<uint4*>(vd + 8) = v1;
         } else {
-            const float* hs = is_v ? a.v_scales : a.k_scales;
-            const float s = hs ? __ldg(hs + h) : (is_v ? a.v_scale : a.k_scale);
+            constexpr bool E5M2 = FMT == FP8KV_CACHE_E5M2;
             uint32_t o[4];
-            codes16<FMT == FP8KV_CACHE_E5M2>(x, s, o);
-            store_codes(static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + row, e0, e1, o);
+            codes16<E5M2>(x, a.k_scales ? __ldg(a.k_scales + h) : a.k_scale, o);
+            store_codes(static_cast<uint8_t*>(a.k_cache) + row, e0, e1, o);
+            unpack(v0, v1, x);
+            codes16<E5M2>(x, a.v_scales ? __ldg(a.v_scales + h) : a.v_scale, o);
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.v_cache) + row + 16 * j) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 }
@@ -441,8 +479,8 @@ __device__ __forceinline__ PageWork find_page(const BlockArgs& a, int lane) {
 // one head of the page (16 rows x D / 16 items), so kThreads / D heads go at a
 // time: load, turn, largest magnitude over the page (shuffles, then shared
 // memory, one barrier), new scale, codes.
-template <int D>
-__global__ void __launch_bounds__(kThreads) rope_append_block_kernel(const BlockArgs a) {
+template <int D, bool PAIRS>
+__global__ void __launch_bounds__(kThreads, 4) rope_append_block_kernel(const BlockArgs a) {
     constexpr int IPR = D / 16;
     constexpr int HPI = kThreads / D;          // heads per iteration
     constexpr int WPH = D / 32;                // warps per head
@@ -461,32 +499,30 @@ __global__ void __launch_bounds__(kThreads) rope_append_block_kernel(const Block
     if (w.cnt == 0) return;
     const Rows& rw = a.rw;
     const Rope& rp = a.rp;
-    fill_table(tab, rp, w.t0, w.cnt, w.pos, rw.num_tokens, tid);
-    __syncthreads();
-    if (rw.q) {
-        const int h0 = static_cast<int>(static_cast<int64_t>(rw.hq) * blockIdx.y / gridDim.y);
-        const int h1 = static_cast<int>(static_cast<int64_t>(rw.hq) * (blockIdx.y + 1) / gridDim.y);
-        const int per_tok = (h1 - h0) * IPR;
-#pragma unroll 2
-        for (int i = tid; i < w.cnt * per_tok; i += kThreads) {
-            const int tok = i / per_tok, rem = i - tok * per_tok;
-            q_item<D>(rw, rp, tab, w.t0, tok, h0 + rem / IPR, rem % IPR);
-        }
-    }
+    auto ready = [&]() {          // the rotation table
+        fill_table(tab, rp, w.t0, w.cnt, w.pos, rw.num_tokens, tid);
+        __syncthreads();
+    };
+    const int64_t y = blockIdx.y, ny = gridDim.y;
+    if (rw.q)
+        q_rows<D, PAIRS>(rw, rp, tab, w.t0, w.cnt, static_cast<int>(rw.hq * y / ny),
+                         static_cast<int>(rw.hq * (y + 1) / ny), tid, ready);
+    else
+        ready();
     if (w.block < 0) return;
-    const int kv0 = static_cast<int>(static_cast<int64_t>(rw.hkv) * blockIdx.y / gridDim.y);
-    const int kv1 = static_cast<int>(static_cast<int64_t>(rw.hkv) * (blockIdx.y + 1) / gridDim.y);
+    const int kv0 = static_cast<int>(rw.hkv * y / ny), kv1 = static_cast<int>(rw.hkv * (y + 1) / ny);
     const int slot = tid / D, row = (tid % D) / IPR, j = tid % IPR;
     const bool is_new = row >= w.r0 && row < w.r0 + w.cnt;
     const int tok = row - w.r0;
     int e0, e1;
-    item_place(rp, j, e0, e1);
+    item_place<PAIRS>(rp, j, e0, e1);
     int it = 0;
     for (int hb = kv0; hb < kv1; hb += HPI, ++it) {
         const int h = hb + slot;
         const bool live = h < kv1;
         const int64_t ph = static_cast<int64_t>(w.block) * rw.hkv + h;
-        float xk[16], xv[16];
+        float x[16];
+        uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;      // (V stays packed: half the registers)
         float mk = 0.f, mv = 0.f, old_k = 0.f, old_v = 0.f;
         if (live && w.r0 > 0) {
             old_k = a.k_scales[ph];
@@ -497,13 +533,13 @@ __global__ void __launch_bounds__(kThreads) rope_append_block_kernel(const Block
             const uint16_t* vs = rw.v + (w.t0 + tok) * rw.v_stride + static_cast<int64_t>(h) * D + 16 * j;
             const uint4 k0 = __ldcs(reinterpret_cast<const uint4*>(ks + e0));
             const uint4 k1 = __ldcs(reinterpret_cast<const uint4*>(ks + e1));
-            const uint4 v0 = __ldcs(reinterpret_cast<const uint4*>(vs));
-            const uint4 v1 = __ldcs(reinterpret_cast<const uint4*>(vs + 8));
-            unpack(k0, k1, xk);
-            unpack(v0, v1, xv);
-            if (j < rp.rot) turn(xk, tab, rp, tok, j);
-            mk = amax16(xk);
-            mv = amax16(xv);
+            v0 = __ldcs(reinterpret_cast<const uint4*>(vs));
+            v1 = __ldcs(reinterpret_cast<const uint4*>(vs + 8));
+            unpack(v0, v1, x);
+            mv = amax16(x);
+            unpack(k0, k1, x);
+            if (j < rp.rot) turn<PAIRS>(x, tab, rp, tok, j);
+            mk = amax16(x);
         }
 #pragma unroll
         for (int off = 16; off; off >>= 1) {
@@ -528,9 +564,10 @@ __global__ void __launch_bounds__(kThreads) rope_append_block_kernel(const Block
         uint8_t* vp = a.v_cache + (ph * kBS + row) * D;
         if (is_new) {
             uint32_t o[4];
-            codes16<false>(xk, sk, o);
+            codes16<false>(x, sk, o);
             store_codes(kp, e0, e1, o);
-            codes16<false>(xv, sv, o);
+            unpack(v0, v1, x);
+            codes16<false>(x, sv, o);
             *reinterpret_cast<uint4*>(vp + 16 * j) = make_uint4(o[0], o[1], o[2], o[3]);
         } else if (row < w.r0) {
             if (!keep_k) requantise(kp + 16 * j, old_k / sk);
@@ -576,13 +613,12 @@ fp8kv_status make_rows(const void* q, int64_t q_stride, void* q_out, const void*
 }
 
 fp8kv_status make_rope(const int32_t* positions, int num_axes, const float* inv_freq, const uint8_t* freq_axis,
-                       int rotary_dim, int rope_style, bool need_positions, Rope* rp) {
+                       int rotary_dim, bool need_positions, Rope* rp) {
     rp->positions = positions;
     rp->inv_freq = inv_freq;
     rp->freq_axis = freq_axis;
     rp->axes = num_axes;
     rp->rot = rotary_dim / 16;
-    rp->pairs = rope_style == FP8KV_ROPE_PAIRS;
     if (rotary_dim == 0) return FP8KV_OK;
     if (!inv_freq || !a4(inv_freq) || (positions && !a4(positions))) return FP8KV_ERR_INVALID_ARG;
     if (!positions && (need_positions || num_axes != 1)) return FP8KV_ERR_INVALID_ARG;
@@ -628,9 +664,23 @@ cudaError_t launch(void (*kernel)(const A), const A& a, int64_t blocks, int spli
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+template <int FMT, bool PAIRS>
+void (*slot_kernel_d(int d))(const SlotArgs) {
+    return d == 64    ? rope_append_kernel<64, FMT, PAIRS>
+           : d == 128 ? rope_append_kernel<128, FMT, PAIRS>
+                      : rope_append_kernel<256, FMT, PAIRS>;
+}
+
 template <int FMT>
-void (*slot_kernel(int d))(const SlotArgs) {
-    return d == 64 ? rope_append_kernel<64, FMT> : d == 128 ? rope_append_kernel<128, FMT> : rope_append_kernel<256, FMT>;
+void (*slot_kernel(int d, bool pairs))(const SlotArgs) {
+    return pairs ? slot_kernel_d<FMT, true>(d) : slot_kernel_d<FMT, false>(d);
+}
+
+template <bool PAIRS>
+void (*block_kernel(int d))(const BlockArgs) {
+    return d == 64    ? rope_append_block_kernel<64, PAIRS>
+           : d == 128 ? rope_append_block_kernel<128, PAIRS>
+                      : rope_append_block_kernel<256, PAIRS>;
 }
 
 }  // namespace rope
@@ -666,7 +716,7 @@ extern "C" fp8kv_status fp8kv_rope_append(const void* q, int64_t q_stride, void*
     fp8kv_status st = make_rows(q, q_stride, q_out, k_new, k_stride, v_new, v_stride, num_tokens, num_q_heads,
                                 num_kv_heads, head_dim, &a.rw);
     if (st != FP8KV_OK) return st;
-    st = make_rope(positions, num_axes, inv_freq, freq_axis, rotary_dim, rope_style, true, &a.rp);
+    st = make_rope(positions, num_axes, inv_freq, freq_axis, rotary_dim, true, &a.rp);
     if (st != FP8KV_OK) return st;
     a.slots = slot_mapping;
     a.k_cache = k_cache;
@@ -681,9 +731,10 @@ extern "C" fp8kv_status fp8kv_rope_append(const void* q, int64_t q_stride, void*
     if (fp8kv::device_sms(&sms) != 0) return FP8KV_ERR_CUDA;
     const int64_t blocks = (num_tokens + kTok - 1) / kTok;
     const int splits = head_splits(blocks, (q ? num_q_heads : 0) + 2 * num_kv_heads, sms);
-    auto kernel = cache_format == FP8KV_CACHE_E4M3   ? slot_kernel<FP8KV_CACHE_E4M3>(head_dim)
-                  : cache_format == FP8KV_CACHE_E5M2 ? slot_kernel<FP8KV_CACHE_E5M2>(head_dim)
-                                                     : slot_kernel<FP8KV_CACHE_BF16>(head_dim);
+    const bool pairs = rope_style == FP8KV_ROPE_PAIRS;
+    auto kernel = cache_format == FP8KV_CACHE_E4M3   ? slot_kernel<FP8KV_CACHE_E4M3>(head_dim, pairs)
+                  : cache_format == FP8KV_CACHE_E5M2 ? slot_kernel<FP8KV_CACHE_E5M2>(head_dim, pairs)
+                                                     : slot_kernel<FP8KV_CACHE_BF16>(head_dim, pairs);
     return launch(kernel, a, blocks, splits, a.rp.rot, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? FP8KV_OK
                : FP8KV_ERR_CUDA;
@@ -718,7 +769,7 @@ extern "C" fp8kv_status fp8kv_rope_append_block(const void* q, int64_t q_stride,
     fp8kv_status st = make_rows(q, q_stride, q_out, k_new, k_stride, v_new, v_stride, num_tokens, num_q_heads,
                                 num_kv_heads, head_dim, &a.rw);
     if (st != FP8KV_OK) return st;
-    st = make_rope(positions, num_axes, inv_freq, freq_axis, rotary_dim, rope_style, false, &a.rp);
+    st = make_rope(positions, num_axes, inv_freq, freq_axis, rotary_dim, false, &a.rp);
     if (st != FP8KV_OK) return st;
     if (!workspace || workspace_bytes < kWorkspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return FP8KV_ERR_WORKSPACE;
@@ -740,9 +791,7 @@ extern "C" fp8kv_status fp8kv_rope_append_block(const void* q, int64_t q_stride,
     const int64_t blocks = q_starts ? num_tokens / kBS + 2 * static_cast<int64_t>(batch) : batch;
     const int64_t pages = q_starts ? (num_tokens + kBS - 1) / kBS : batch;
     const int splits = head_splits(pages, (q ? num_q_heads : 0) + 2 * num_kv_heads, sms);
-    auto kernel = head_dim == 64    ? rope_append_block_kernel<64>
-                  : head_dim == 128 ? rope_append_block_kernel<128>
-                                    : rope_append_block_kernel<256>;
+    auto kernel = rope_style == FP8KV_ROPE_PAIRS ? block_kernel<true>(head_dim) : block_kernel<false>(head_dim);
     return launch(kernel, a, blocks, splits, a.rp.rot, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? FP8KV_OK
                : FP8KV_ERR_CUDA;
