@@ -377,15 +377,34 @@ __device__ __forceinline__ float least_power(float amax) {
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// The largest finite magnitude of an item.
+// The largest finite magnitude of an item.  (fmaxf passes over NaN; an
+// infinity sends the item round again.)
 __device__ __forceinline__ float amax16(const float (&x)[16]) {
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float v = fabsf(x[i]);
-        m = fmaxf(m, v < INFINITY ? v : 0.f);
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(x[i]));
+    if (m == INFINITY) {
+        m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
     }
     return m;
+}
+
+// codes16 of E4M3 under a page's scale.  Most are powers of two, where the
+// product with the reciprocal is the quotient, exactly, and a quarter of the
+// instructions.
+__device__ __forceinline__ void page_codes16(const float (&x)[16], float s, uint32_t (&o)[4]) {
+    const uint32_t b = __float_as_uint(s), e = b >> 23;
+    if ((b & 0x7FFFFFu) == 0 && e >= 1 && e <= 253) {
+        const float r = __uint_as_float((254u - e) << 23);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] = static_cast<uint32_t>(f32x2_to_e4m3x2_satfinite(x[4 * i] * r, x[4 * i + 1] * r)) |
+                   (static_cast<uint32_t>(f32x2_to_e4m3x2_satfinite(x[4 * i + 2] * r, x[4 * i + 3] * r)) << 16);
+    } else {
+        codes16<false>(x, s, o);
+    }
 }
 
 // Codes of an older row's 16-element chunk from scale `from` to scale `to`.
@@ -564,10 +583,10 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_block_kernel(const Bl
         uint8_t* vp = a.v_cache + (ph * kBS + row) * D;
         if (is_new) {
             uint32_t o[4];
-            codes16<false>(x, sk, o);
+            page_codes16(x, sk, o);
             store_codes(kp, e0, e1, o);
             unpack(v0, v1, x);
-            codes16<false>(x, sv, o);
+            page_codes16(x, sv, o);
             *reinterpret_cast<uint4*>(vp + 16 * j) = make_uint4(o[0], o[1], o[2], o[3]);
         } else if (row < w.r0) {
             if (!keep_k) requantise(kp + 16 * j, old_k / sk);
