@@ -539,8 +539,11 @@ _BF16, _U8, _I32, _F32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
 def _ptr(t, dtype, dev, name):
     """Device pointer of a contiguous CUDA tensor on device `dev` (the current
     one: the library launches on it)."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.get_device() == dev:
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _dev(t, dtype, name)
     raise ValueError("%s is on %s, not on the current device cuda:%d" % (name, t.device, dev))
 

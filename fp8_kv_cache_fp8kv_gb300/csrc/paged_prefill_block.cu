@@ -1161,17 +1161,21 @@ static cudaError_t launch_with(void (*kernel)(const Args), std::atomic<uint64_t>
 }
 
 // Whether a kernel is launched with the registers that its warpgroups' shares
-// add up to: with fewer an increase would never be granted.
-static bool launched_with(void (*kernel)(const Args), int regs) {
+// add up to: with fewer an increase would never be granted.  Asked until the
+// answer is yes.
+static bool launched_with(void (*kernel)(const Args), int regs, std::atomic<bool>& known) {
+    if (known.load(std::memory_order_relaxed)) return true;
     cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, kernel) == cudaSuccess && at.numRegs >= regs;
+    if (cudaFuncGetAttributes(&at, kernel) != cudaSuccess || at.numRegs < regs) return false;
+    known.store(true, std::memory_order_relaxed);
+    return true;
 }
 
 template <int D, int REP>
 static cudaError_t launch_one_rep(const Args& a, dim3 grid, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    static const bool regs_ok = launched_with(paged_prefill_one_kernel<D, REP>, one::kRegs);
-    if (!regs_ok) return cudaErrorInvalidConfiguration;
+    static std::atomic<bool> known{false};
+    if (!launched_with(paged_prefill_one_kernel<D, REP>, one::kRegs, known)) return cudaErrorInvalidConfiguration;
     return launch_with(paged_prefill_one_kernel<D, REP>, done, OneGeo<D>::SMEM + 1024, grid, one::kThreads, a, s);
 }
 
@@ -1196,8 +1200,8 @@ static cudaError_t launch_block_g(int kind, const Args& a, int batch, cudaStream
     } else {
         if constexpr (D < 256) {
             static std::atomic<uint64_t> done{0};
-            static const bool regs_ok = launched_with(paged_prefill_two_kernel<D>, two::kRegs);
-            if (!regs_ok) return cudaErrorInvalidConfiguration;
+            static std::atomic<bool> known{false};
+            if (!launched_with(paged_prefill_two_kernel<D>, two::kRegs, known)) return cudaErrorInvalidConfiguration;
             const int pairs = (a.tiles + two::kTiles - 1) / two::kTiles;
             e = launch_with(paged_prefill_two_kernel<D>, done, static_cast<size_t>(TwoGeo<D>::SMEM) + 1024,
                             dim3(static_cast<unsigned>(pairs * a.splits), hkv, bz), two::kThreads, a, s);

@@ -281,7 +281,7 @@ template <int D, int FMT, bool PAIRS>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const SlotArgs a) {
     constexpr int IPR = D / 16;   // items per row
     extern __shared__ float4 tab[];
-    __shared__ int64_t slot_sh[kTok];
+    __shared__ int64_t row_sh[kTok];   // the token's row of cache head 0, -1: not written
     griddep_launch_dependents();
     griddep_wait();               // the inputs and the cache may be the previous grid's
     const Rows& rw = a.rw;
@@ -291,8 +291,8 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const SlotArgs a)
     auto ready = [&]() {          // the rotation table and the slots
         fill_table(tab, a.rp, t0, cnt, 0, rw.num_tokens, tid);
         if (tid < cnt) {
-            const int64_t s = __ldg(a.slots + t0 + tid);
-            slot_sh[tid] = s < a.num_slots ? s : -1;
+            const int64_t s = __ldg(a.slots + t0 + tid), blk = s / a.block_size;
+            row_sh[tid] = s >= 0 && s < a.num_slots ? blk * rw.hkv * a.block_size + (s - blk * a.block_size) : -1;
         }
         __syncthreads();
     };
@@ -309,8 +309,8 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const SlotArgs a)
         int tok, h, j;
         item_of<IPR>(i, heads, inv, tok, h, j);
         h += kv0;
-        const int64_t slot = slot_sh[tok];
-        if (slot < 0) continue;
+        const int64_t row0 = row_sh[tok];
+        if (row0 < 0) continue;
         int e0, e1;
         item_place<PAIRS>(a.rp, j, e0, e1);
         const uint16_t* ks = rw.k + (t0 + tok) * rw.k_stride + static_cast<int64_t>(h) * D;
@@ -319,8 +319,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const SlotArgs a)
         uint4 k1 = __ldcs(reinterpret_cast<const uint4*>(ks + e1));
         const uint4 v0 = __ldcs(reinterpret_cast<const uint4*>(vs));
         const uint4 v1 = __ldcs(reinterpret_cast<const uint4*>(vs + 8));
-        const int64_t blk = slot / a.block_size, off = slot - blk * a.block_size;
-        const int64_t row = ((blk * rw.hkv + h) * a.block_size + off) * D;
+        const int64_t row = (row0 + static_cast<int64_t>(h) * a.block_size) * D;
         float x[16];
         unpack(k0, k1, x);
         if (j < a.rp.rot) turn<PAIRS>(x, tab, a.rp, tok, j);
@@ -544,8 +543,8 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_block_kernel(const Bl
         uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;      // (V stays packed: half the registers)
         float mk = 0.f, mv = 0.f, old_k = 0.f, old_v = 0.f;
         if (live && w.r0 > 0) {
-            old_k = a.k_scales[ph];
-            old_v = a.v_scales[ph];
+            old_k = __ldcg(a.k_scales + ph);   // (past L1: the heads beside it are written by other CTAs)
+            old_v = __ldcg(a.v_scales + ph);
         }
         if (live && is_new) {
             const uint16_t* ks = rw.k + (w.t0 + tok) * rw.k_stride + static_cast<int64_t>(h) * D;
