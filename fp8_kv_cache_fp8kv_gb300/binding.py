@@ -552,19 +552,22 @@ def _opt(t, dtype, dev, name):
     return None if t is None else _ptr(t, dtype, dev, name)
 
 
-def _rows(t, heads, head_dim, dev, name):
-    """(pointer, token stride in elements) of bf16 [T, heads, head_dim] whose
-    tokens may lie apart (a slice of a fused projection's output)."""
+def _rows(t, tokens, heads, head_dim, dev, name):
+    """(pointer, token stride in elements) of bf16 [tokens, heads, head_dim]
+    whose tokens may lie apart (a slice of a fused projection's output)."""
+    try:
+        step, head, one = t.stride()
+        if t.dtype is _BF16 and t.get_device() == dev and one == 1 and (head == head_dim or heads == 1):
+            return t.data_ptr(), (step if tokens > 1 else heads * head_dim)
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
     if t.dtype is not _BF16:
         raise TypeError("%s must be %s, got %s" % (name, _BF16, t.dtype))
     if t.get_device() != dev:
         raise ValueError("%s is on %s, not on the current device cuda:%d" % (name, t.device, dev))
-    st = t.stride()
-    if st[2] != 1 or (heads > 1 and st[1] != head_dim):
-        raise ValueError("%s: the heads of a token must be contiguous" % name)
-    return t.data_ptr(), (st[0] if t.shape[0] > 1 else heads * head_dim)
+    raise ValueError("%s: the heads of a token must be contiguous" % name)
 
 
 def _where(stream, cache):
@@ -595,23 +598,23 @@ def _rope_args(positions, inv_freq, freq_axis, head_dim, tokens, dev):
 
 
 def _append_rows(q, k_new, v_new, q_out, hkv, d, dev):
-    """Shapes and pointers of the token rows: (q, q_stride, q_out, k, k_stride, v, v_stride), query heads."""
+    """(tokens, query heads, (q, q_stride, q_out, k, k_stride, v, v_stride)) of the token rows."""
     shape = k_new.shape
     if len(shape) != 3 or shape[1] != hkv or shape[2] != d or v_new.shape != shape:
         raise ValueError("k_new/v_new must be [T, Hkv, D] matching the cache")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out come together")
-    hq, qp, qs, qo = 0, None, 0, None
-    if q is not None:
-        qshape = q.shape
-        if len(qshape) != 3 or qshape[0] != shape[0] or qshape[2] != d or q_out.shape != qshape:
-            raise ValueError("q and q_out must be [T, Hq, D]")
-        hq = qshape[1]
-        qp, qs = _rows(q, hq, d, dev, "q")
-        qo = _ptr(q_out, _BF16, dev, "q_out")
-    kp, ks = _rows(k_new, hkv, d, dev, "k_new")
-    vp, vs = _rows(v_new, hkv, d, dev, "v_new")
-    return (qp, qs, qo, kp, ks, vp, vs), hq
+    T = shape[0]
+    kp, ks = _rows(k_new, T, hkv, d, dev, "k_new")
+    vp, vs = _rows(v_new, T, hkv, d, dev, "v_new")
+    if q is None:
+        return T, 0, (None, 0, None, kp, ks, vp, vs)
+    qshape = q.shape
+    if len(qshape) != 3 or qshape[0] != T or qshape[2] != d or q_out.shape != qshape:
+        raise ValueError("q and q_out must be [T, Hq, D]")
+    hq = qshape[1]
+    qp, qs = _rows(q, T, hq, d, dev, "q")
+    return T, hq, (qp, qs, _ptr(q_out, _BF16, dev, "q_out"), kp, ks, vp, vs)
 
 
 def fp8kv_rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, q_out, k_cache, v_cache, k_scale=1.0,
@@ -624,8 +627,7 @@ def fp8kv_rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, q_out,
     [num_blocks, Hkv, bs, D] (bf16 for CACHE_BF16).  q and q_out may be None."""
     nb, hkv, bs, d = k_cache.shape
     dev, st = _where(stream, k_cache)
-    rows, hq = _append_rows(q, k_new, v_new, q_out, hkv, d, dev)
-    T = k_new.shape[0]
+    T, hq, rows = _append_rows(q, k_new, v_new, q_out, hkv, d, dev)
     if v_cache.shape != k_cache.shape or slot_mapping.numel() != T:
         raise ValueError("cache or slot_mapping shape mismatch")
     if (k_scales is not None and k_scales.numel() != hkv) or (v_scales is not None and v_scales.numel() != hkv):
@@ -676,10 +678,10 @@ def fp8kv_rope_append_block(q, k_new, v_new, positions, inv_freq, q_out, k_cache
     token's place in its sequence.  Other shapes as fp8kv_rope_append and
     fp8kv_paged_decode."""
     nb, hkv, bs, d = k_cache.shape
-    T, B = k_new.shape[0], seq_lens.numel()
+    B = seq_lens.numel()
     mb = _block_shapes(k_cache, v_cache, k_scales, v_scales, block_tables, B)
     dev, st = _where(stream, k_cache)
-    rows, hq = _append_rows(q, k_new, v_new, q_out, hkv, d, dev)
+    T, hq, rows = _append_rows(q, k_new, v_new, q_out, hkv, d, dev)
     if q_starts is None:
         if T != B:
             raise ValueError("without q_starts there is one row per sequence")
