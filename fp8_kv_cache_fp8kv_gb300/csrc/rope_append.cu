@@ -444,9 +444,25 @@ __device__ __forceinline__ PageWork find_page(const BlockArgs& a, int lane) {
     w.r0 = w.pos = 0;
     w.block = -1;
     const int64_t x = blockIdx.x;
-    int b;
-    int64_t q0, n, j;
+    // a sequence of n tokens from packed row q0 and length L that the documented bounds allow
+    auto fits = [&](int64_t q0, int64_t n, int L) {
+        return n >= 0 && L >= n && L <= a.max_seq_len && q0 >= 0 && q0 + n <= a.rw.num_tokens;
+    };
+    auto report = [&]() {
+        if (lane == 0) atomicCAS(a.err, 0u, static_cast<uint32_t>(FP8KV_ERR_INVALID_ARG));
+    };
+    int b = static_cast<int>(x);
+    int64_t q0 = x, n = 1, j = 0;
     if (a.q_starts) {
+        // starts that fall could hide a sequence from the search, so CTA b looks
+        // at sequence b whatever it finds (there are at least 2 CTAs a sequence)
+        int own0 = 0, own1 = 0, own_len = 0;
+        const bool own = x < a.batch;
+        if (own) {
+            own0 = __ldg(a.q_starts + x);
+            own1 = __ldg(a.q_starts + x + 1);
+            own_len = __ldg(a.seq_lens + x);
+        }
         int lo = 0, cnt = a.batch;
         while (cnt > 1) {
             const int step = (cnt + 31) / 32;
@@ -462,31 +478,27 @@ __device__ __forceinline__ PageWork find_page(const BlockArgs& a, int lane) {
         q0 = __ldg(a.q_starts + b);
         n = __ldg(a.q_starts + b + 1) - q0;
         j = x - (q0 / kBS + 2 * static_cast<int64_t>(b));
-    } else {
-        b = static_cast<int>(x);
-        q0 = x;
-        n = 1;
-        j = 0;
+        if (own && own0 != own1 && !fits(own0, static_cast<int64_t>(own1) - own0, own_len)) report();
     }
     const int L = __ldg(a.seq_lens + b);
     if (!a.q_starts && L == 0) return w;    // an empty slot of a padded batch
     if (n == 0) return w;
-    if (n < 0 || L < n || L > a.max_seq_len || q0 < 0 || q0 + n > a.rw.num_tokens) {
-        if (lane == 0) atomicCAS(a.err, 0u, static_cast<uint32_t>(FP8KV_ERR_INVALID_ARG));
+    if (!fits(q0, n, L)) {
+        report();
         return w;
     }
     const int p0 = static_cast<int>(L - n);
     const int64_t page = p0 / kBS + j;
     if (j < 0 || page > (L - 1) / kBS) return w;
     const int first = static_cast<int>(page) * kBS;
-    const int start = max(p0, first), end = min(L, first + kBS);
-    w.cnt = end - start;
+    const int start = max(p0, first);
     w.r0 = start - first;
+    w.cnt = min(L - first, kBS) - w.r0;
     w.pos = start;
     w.t0 = q0 + (start - p0);
     w.block = __ldg(a.block_tables + static_cast<int64_t>(b) * a.max_blocks_per_seq + page);
     if (w.block < 0 || w.block >= a.num_blocks) {
-        if (lane == 0) atomicCAS(a.err, 0u, static_cast<uint32_t>(FP8KV_ERR_INVALID_ARG));
+        report();
         w.block = -1;
     }
     return w;

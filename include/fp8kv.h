@@ -525,8 +525,8 @@ fp8kv_status fp8kv_rope_append(const void* q, int64_t q_stride, void* q_out, con
  *   num_tokens          rows of q, k_new, v_new and positions
  *   positions           null with num_axes 1: each token's place in its sequence
  *   block_tables        int32 [batch][max_blocks_per_seq], as fp8kv_paged_decode.
- *                       The pages written must belong to one sequence each:
- *                       a page that two sequences append to in one call gets
+ *                       A page written must be in one place of one sequence's
+ *                       row only: a page that one call appends to twice gets
  *                       unspecified codes and scales.
  *   seq_lens            int32 [batch] on the device
  *   q_starts            int32 [batch + 1] on the device, non-decreasing, or
@@ -577,6 +577,10 @@ fp8kv_status fp8kv_paged_decode_block(const void* q, const uint8_t* k_cache, con
  * fp8kv_paged_prefill over a block-scaled cache (append the chunk first, with
  * fp8kv_rope_append_block).  All other arguments, the workspace
  * (fp8kv_paged_prefill_workspace_size) and the errors as fp8kv_paged_prefill.
+ * What a row may not attend does not reach it, with one exception, as in
+ * fp8kv_paged_prefill: a NaN code in V makes NaN of its dimension in every
+ * row that shares a tile (up to 256 rows: token, query head) with one that
+ * attends it, since a masked weight of zero still multiplies it.
  */
 fp8kv_status fp8kv_paged_prefill_block(const void* q, int64_t num_q_tokens, const uint8_t* k_cache,
                                        const uint8_t* v_cache, const float* k_scales, const float* v_scales,

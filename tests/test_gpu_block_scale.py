@@ -267,3 +267,41 @@ def test_rescaled_rows_of_a_short_chunk():
             q = randn((n, hq, d), 5).abs()
             out = f64(run_prefill(c, q.cuda(), starts, n, d ** -0.5))
             check_rows(out, c, 0, f64(q), list(range(900 - n, 900)), d ** -0.5, 0, True, (d, n, up))
+
+
+@pytest.mark.parametrize("hq,hkv,d,n", [(4, 1, 128, 7), (4, 1, 128, 25), (4, 2, 128, 200), (8, 1, 64, 40), (4, 1, 256, 70)])
+@pytest.mark.parametrize("window", [0, 60])
+def test_nan_keys_stay_out_of_the_rows_that_do_not_attend_them(hq, hkv, d, n, window):
+    """A key of NaN codes inside a chunk: the rows before it, and those whose window has passed it, come out as they
+    do without it; the rows that attend it are NaN."""
+    L, t = 400, 400 - n // 2
+    c = Cache(hkv, d, [L], seed=d + n).cuda()
+    q = randn((n, hq, d), 4)
+    starts = torch.tensor([0, n], dtype=torch.int32).cuda()
+    c.gk[int(c.tables[0, t // 16]), :, t % 16] = 0x7F
+    out = f64(run_prefill(c, q.cuda(), starts, n, 0.1, window))
+    dec = f64(run_decode(c, q[-1:].cuda(), 0.1, window))
+    attends = [t <= p and (window == 0 or p - t < window) for p in range(L - n, L)]
+    for i, (p, hit) in enumerate(zip(range(L - n, L), attends)):
+        if hit:
+            assert np.isnan(out[i]).all()
+        else:
+            check_rows(out[i:i + 1], c, 0, f64(q[i:i + 1]), [p], 0.1, window, True, p)
+    assert np.isnan(dec).all() == attends[-1]
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (16, 2, 64), (4, 1, 256)])
+@pytest.mark.parametrize("counts", [[3, 1], [90, 40]])
+def test_prefill_leaves_rows_that_no_sequence_has(hq, hkv, d, counts):
+    """Rows of q before the first sequence and behind the last: out keeps what it held."""
+    c = Cache(hkv, d, [300, 40], seed=d).cuda()
+    first, T = 5, 5 + sum(counts) + 9
+    q = randn((T, hq, d), 3)
+    starts = torch.tensor([first, first + counts[0], first + sum(counts)], dtype=torch.int32).cuda()
+    out = torch.full((T, hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = f64(run_prefill(c, q.cuda(), starts, max(counts), 0.1, out=out))
+    assert (out[:first] == 7).all() and (out[first + sum(counts):] == 7).all()
+    at = first
+    for b, n in enumerate(counts):
+        check_rows(out[at:at + n], c, b, f64(q[at:at + n]), list(range(c.lens[b] - n, c.lens[b])), 0.1, 0, True, b)
+        at += n

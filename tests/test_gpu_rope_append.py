@@ -481,3 +481,69 @@ def test_captured_append_and_decode_advance_with_their_lengths():
         for b in range(2):
             check_rows(f64(out[b:b + 1]), c, b, f64(qo[b:b + 1]), [c.lens[b] - 1], 0.1, 0, False, (i, b))
     assert fk.fp8kv_read_error(ws) == 0
+
+
+@pytest.mark.parametrize("at", [1, 2, 31, 32, 33, 64, 68])
+def test_starts_that_fall_are_reported_and_nothing_out_of_range_is_written(at):
+    """Whichever sequence the starts fall at, also where the search for a CTA's sequence would pass it by."""
+    hkv, d, B, n = 1, 64, 70, 20
+    for start in (0, 3, n * at - 1, n * at - 40):
+        if start < 0:
+            continue
+        c = Cache(hkv, d, [48] * B, seed=at).cuda()
+        starts = [n * i for i in range(B + 1)]
+        starts[at + 1] = start
+        ws = fk.alloc_append_workspace()
+        _, k, v = _fused(n * B, 1, hkv, d, 4)
+        _block_append(c, None, k, v, None, None, starts, ws)
+        assert fk.fp8kv_read_error(ws) == 1
+        owned = {int(x) for row in c.tables for x in row}
+        before = _copy(c)
+        c.pull()
+        for blk in set(range(c.nb)) - owned:
+            assert np.array_equal(c.k[blk], before.k[blk]) and np.array_equal(c.v[blk], before.v[blk])
+
+
+def test_appends_and_attention_on_two_streams_at_once():
+    """Two sets of sequences of one cache, each with a stream and workspaces of its own, their calls in flight
+    together: the outcome of each is what it is alone."""
+    hq, hkv, d, steps = 16, 4, 128, 30
+    freq = _freq(d).cuda()
+    kw = dict(hkv=hkv, d=d, hist=[600, 37, 255, 1200], counts=[40] * 4, seed=8)
+
+    def run(order):
+        c = _history(**kw).cuda()
+        outs, streams = [], []
+        for half in order:
+            rows = slice(2 * half, 2 * half + 2)
+            q, k, v = _fused(80, hq, hkv, d, 20 + half)
+            gt, gl = c.gt[rows].contiguous(), c.gl[rows].contiguous()
+            gs = torch.tensor([0, 40, 80], dtype=torch.int32).cuda()
+            ws = fk.alloc_prefill_workspace(2, 40, c.mb * 16, hq, hkv, d)
+            wsd = fk.alloc_workspace(2, hq, hkv, d, c.mb * 16)
+            qo = torch.empty((80, hq, d), dtype=torch.bfloat16, device="cuda")
+            out, dec = torch.full_like(qo, float("nan")), torch.full_like(qo[:2], float("nan"))
+            outs.append((half, qo, out, dec, ws, wsd, gt, gl, gs, q, k, v))
+            streams.append(torch.cuda.Stream())
+        torch.cuda.synchronize()
+        for (half, qo, out, dec, ws, wsd, gt, gl, gs, q, k, v), st in zip(outs, streams):
+            with torch.cuda.stream(st):
+                fk.fp8kv_rope_append_block(q, k, v, None, freq, qo, c.gk, c.gv, c.gks, c.gvs, gt, gl, gs, c.mb * 16, ws)
+                for _ in range(steps):
+                    fk.fp8kv_paged_prefill_block(qo, c.gk, c.gv, c.gks, c.gvs, gt, gl, gs, 40, c.mb * 16, 0.1, 0, out, ws)
+                    fk.fp8kv_paged_decode_block(qo[:2], c.gk, c.gv, c.gks, c.gvs, gt, gl, c.mb * 16, 0.1, 0, dec, wsd)
+            if len(order) == 1:
+                st.synchronize()
+        torch.cuda.synchronize()
+        for o in outs:
+            assert fk.fp8kv_read_error(o[4]) == 0 and fk.fp8kv_read_error(o[5]) == 0
+        c.pull()
+        pages = {o[0]: [int(x) for r in (2 * o[0], 2 * o[0] + 1) for x in c.tables[r, : -(-c.lens[r] // 16)]] for o in outs}
+        return {o[0]: (bits(o[1]), bits(o[2]), bits(o[3]), c.k[pages[o[0]]], c.v[pages[o[0]]], c.ks[pages[o[0]]])
+                for o in outs}
+
+    alone = {**run([0]), **run([1])}
+    both = run([0, 1])
+    for half in (0, 1):
+        for x, y in zip(alone[half], both[half]):
+            assert np.array_equal(x, y)
