@@ -224,6 +224,17 @@ constexpr float kMaxSum = 256.f;
 //     combined through shared memory at the end.
 // Every mbarrier wait is bounded, and the first role to give up ends the
 // others' waits (abort flag), as in the two-tile kernel.
+//
+// Measured: 8 x 20K, 32 over 8 heads, d = 128, 9 new tokens: 116 us, 330 MB
+// read at 2.85 TB/s (the hand-overs and MMAs alone take 83, of which 27 are the
+// three waves' first stages); 4 x 9K, 777 new tokens, window 512, 8 over 1 heads, d = 256:
+// 42 us, 310 TFLOP/s, two waves of one CTA per SM.  With 2 splits a unit and one
+// wave (128 CTAs) the first took 127.  REP by the rows a chunk may have: 8 x 20K,
+// 8 tokens (32 rows): 99 us with four copies, 112 with two or one; 8 x 16K, d = 64,
+// 4 tokens (32 rows): 70, 82 and 86, 8 tokens (64 rows): 82 with two, 87 with one;
+// d = 256, 16 x 9K, 8 tokens (64 rows): 38 and 40; without difference at 64 rows
+// of d = 128 (114.8).  Against the two-tile kernel, 8 x 20K: 33 tokens (two tiles)
+// 228 us and 186 there.
 namespace one {
 constexpr int kConvWarp0 = 4;              // warps 4-11 convert
 constexpr int kConv = 8 * 32;
@@ -715,18 +726,31 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
 //     that a stage has landed and that the slot to refill has been read), block
 //     ids a stage ahead of that, then the conversion into the K tile or into one
 //     of two V^T tiles;
-//   * one thread of warp 16 issues the MMAs, tile by tile in turn: once P of
-//     stage s is in, O += P V, then S = Q K^T of stage s + 1 over the same
-//     columns (the MMAs of one thread run in issue order);
+//   * one thread of warp 16 issues the MMAs, tile by tile in turn: once P of the
+//     first 64 keys of stage s is in, its half of O += P V; once P of the others
+//     is, their half, then S = Q K^T of stage s + 1 over the same columns (the
+//     MMAs of one thread run in issue order);
 //   * warp 17 prepares the page scales, a stage ahead;
 //   * warps 0-3 and 4-7 (a warpgroup per tile, thread = row = TMEM lane) weigh
 //     the stage in two halves of 64 keys as the one-tile kernel does -- under
 //     the reference the row has, one read of S, P over S already read.
 // The two tiles ping-pong: while one tile's warps weigh, the tensor cores run
-// the other's MMAs.  Stages of 64 keys with two S buffers a tile measured 1819
-// against 1464 us (8 x 20K, chunks of 512 tokens): at N = 64 the score MMAs
-// read Q from shared memory twice as often for the same work, and the second
-// buffer did not make up for it.
+// the other's MMAs.
+//
+// What bounds it: the round trip of a tile -- its warps weigh a stage (about
+// 2600 cycles, of which each of the two reads of S waits for the MMAs in
+// flight), then the tensor cores run its MMAs -- next to which they are 46%
+// busy.  8 x 20K, chunks of 512 tokens (1.35 TFLOP): 1375 us, 983 TFLOP/s.  The
+// MMAs and hand-overs alone take 980 us, all but the softmax 1065.  The same with
+//   * one hand-over of P a stage, not two: 1433 us;
+//   * stages of 64 keys with two S buffers a tile: 1819 us when this kernel took
+//     1464.  At N = 64 the score MMAs read Q from shared memory twice as often
+//     for the same work.  (Scores of 128 keys as two MMAs of N = 64, the second
+//     half's issued while the first half is weighed: 1700 us);
+//   * 32 keys at a time, the next 32 being read meanwhile: 1590 us;
+//   * two threads a row, each half of the keys (16 softmax warps, one read of S a
+//     stage, at 96 registers): 1412 us when this kernel took 1433; the reads of S
+//     take longer the more warps read.
 namespace two {
 constexpr int kTiles = 2;
 constexpr int kKWarp0 = 8, kVWarp0 = 12;   // warps 8-11 convert K, 12-15 V
@@ -765,7 +789,7 @@ __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(con
     constexpr int KEYS = Tg::KEYS, PAGES = Tg::PAGES, HK = KEYS / 2;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t k_full, k_empty, v_full[2], v_empty[2], c_full[2], c_empty[2];
-    __shared__ uint64_t s_full[kTiles], p_full[kTiles], done_bar;
+    __shared__ uint64_t s_full[kTiles], p_half[kTiles], p_full[kTiles], h_done[kTiles], done_bar;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_sh;
     __shared__ float4 psc[2][PAGES];
@@ -785,7 +809,9 @@ __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(con
         }
         for (int i = 0; i < kTiles; ++i) {
             mbar_init(&s_full[i], 1);
+            mbar_init(&p_half[i], 128);
             mbar_init(&p_full[i], 128);
+            mbar_init(&h_done[i], 1);
         }
         mbar_init(&done_bar, 1);
         abort_sh = 0;
@@ -889,7 +915,8 @@ __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(con
             if (!(t0 + KEYS <= sp1 * kBS && t0 + KEYS - 1 <= wpos0 && t0 >= wlo1))
                 mask_keys<HK>(sv, t0 + HK * hf, lq, pq, sp1 * kBS);
         };
-        for (int st = 0; st < nst; ++st) {
+        bool ok = true;
+        for (int st = 0; st < nst && ok; ++st) {
             // S of stage st is in; its commit also covers the P V of stage
             // st - 1, so O is complete and P's columns are free.  (The waits'
             // result is made warp-uniform: the TMEM loads are collective.)
@@ -947,7 +974,13 @@ __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(con
                                 m = mn;
                             }
                             if (__any_sync(0xffffffffu, held)) {
-                                // O = O * alpha for the warp's rows (16 columns at a time: the scores are in registers)
+                                // O = O * alpha for the warp's rows (16 columns at a time: the scores are in
+                                // registers), once the first half's value MMAs are in
+                                if (hf == 1) {
+                                    ok = __all_sync(0xffffffffu, wait_or_abort(&h_done[ti], st & 1, a.wait_ns, abort_flag));
+                                    if (!ok) break;
+                                    tc::fence_after_sync();
+                                }
 #pragma unroll 1
                                 for (int c = 0; c < D / 16; ++c) {
                                     float x[16];
@@ -956,26 +989,6 @@ __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(con
 #pragma unroll
                                     for (int j = 0; j < 16; ++j) x[j] *= alpha;
                                     tc::st16(trow + Tg::OC + 16 * c, x);
-                                }
-                                // ... and for the second half the first half's
-                                // weights, which are f16 already: one more
-                                // rounding of 2^-11, where a reference moves
-                                // within a stage
-                                if (hf == 1) {
-                                    tc::wait_st();
-#pragma unroll 1
-                                    for (int c = 0; c < HK / 32; ++c) {
-                                        float x[16];
-                                        tc::ld16(trow + 16 * c, x);
-                                        tc::wait_ld(x);
-#pragma unroll
-                                        for (int j = 0; j < 16; ++j) {
-                                            const uint32_t y = __float_as_uint(x[j]);
-                                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y));
-                                            x[j] = __uint_as_float(pack_f16x2(f.x * alpha, f.y * alpha));
-                                        }
-                                        tc::st16(trow + 16 * c, x);
-                                    }
                                 }
                             }
                         }
@@ -986,7 +999,14 @@ __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(con
                         if (!look) break;
                     }
                     lst += ls;
+                    if (!ok) break;
+                    if (hf == 0) {             // P of the first half may go
+                        tc::wait_st();
+                        tc::fence_before_sync();
+                        mbar_arrive(&p_half[ti]);
+                    }
                 }
+                if (!ok) break;
                 l += lst;
             }
             __syncwarp();
@@ -994,6 +1014,8 @@ __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(con
             if (warp_rows) {
                 tc::wait_st();
                 tc::fence_before_sync();
+            } else {
+                mbar_arrive(&p_half[ti]);
             }
             mbar_arrive(&p_full[ti]);      // P (and the rescaled O) are in TMEM
         }
@@ -1073,7 +1095,7 @@ __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(con
         for (int st = 0; st < nst && ok; ++st)
             for (int i = 0; i < kTiles && ok; ++i) {
                 const int j = st & 1;
-                ok = wait_or_abort(&p_full[i], st & 1, a.wait_ns, abort_flag) &&
+                ok = wait_or_abort(&p_half[i], st & 1, a.wait_ns, abort_flag) &&
                      (i > 0 || wait_or_abort(&v_full[j], (st >> 1) & 1, a.wait_ns, abort_flag));
                 if (!ok) break;
                 tc::fence_after_sync();
@@ -1081,7 +1103,14 @@ __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(con
                 const uint32_t pc = tm + i * Tg::TC;
                 const uint64_t vd = tc::desc_at(vd0, j * Tg::VTB);
 #pragma unroll
-                for (int ks = 0; ks < KEYS / 16; ++ks)
+                for (int ks = 0; ks < KEYS / 32; ++ks)
+                    tc::mma_f16_ts(pc + Tg::OC, pc + ks * 8, tc::desc_at(vd, (ks >> 2) * Tg::VAT + (ks & 3) * 32), id_o, 1);
+                tc::commit(&h_done[i]);
+                ok = wait_or_abort(&p_full[i], st & 1, a.wait_ns, abort_flag);
+                if (!ok) break;
+                tc::fence_after_sync();
+#pragma unroll
+                for (int ks = KEYS / 32; ks < KEYS / 16; ++ks)
                     tc::mma_f16_ts(pc + Tg::OC, pc + ks * 8, tc::desc_at(vd, (ks >> 2) * Tg::VAT + (ks & 3) * 32), id_o, 1);
                 // the V^T tile is free when both tiles' value MMAs complete
                 if (i == kTiles - 1) tc::commit(&v_empty[j]);

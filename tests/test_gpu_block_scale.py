@@ -305,3 +305,20 @@ def test_prefill_leaves_rows_that_no_sequence_has(hq, hkv, d, counts):
     for b, n in enumerate(counts):
         check_rows(out[at:at + n], c, b, f64(q[at:at + n]), list(range(c.lens[b] - n, c.lens[b])), 0.1, 0, True, b)
         at += n
+
+
+@pytest.mark.parametrize("hq,hkv,d,n", [(4, 1, 128, 70), (8, 1, 64, 40), (1, 1, 128, 300), (16, 1, 64, 17)])
+@pytest.mark.parametrize("window", [0, 100])
+def test_rescaled_rows_of_a_long_chunk(hq, hkv, d, n, window):
+    """The same for chunks of several query tiles: scores that grow from page to page move the maximum in both halves
+    of every stage, behind value products that are on their way."""
+    for grow in (lambda p: 0.5 * (p + 1), lambda p: 0.5 * (57 - p), lambda p: 8.0 if p % 8 == 5 else 0.25 + 0.1 * p):
+        c = Cache(hkv, d, [900], seed=3, spread=0.0)
+        for p in range(-(-900 // 16)):
+            c.ks[c.tables[0, p]] *= grow(p)
+        c.k = (c.k & 0x7F).astype(np.uint8)
+        c.cuda()
+        starts = torch.tensor([0, n], dtype=torch.int32).cuda()
+        q = randn((n, hq, d), 5).abs()
+        out = f64(run_prefill(c, q.cuda(), starts, n, d ** -0.5, window))
+        check_rows(out, c, 0, f64(q), list(range(900 - n, 900)), d ** -0.5, window, True, (d, n))
