@@ -19,7 +19,7 @@
 //    and cut into one equal contiguous range per CTA (2 CTAs per SM), so all
 //    CTAs finish together whatever the mix of sequence lengths.  A CTA walks
 //    the units its range overlaps ("segments").
-//  * Tensor-core engine (the default, stream_decode_kernel): no producer
+//  * Tensor-core engine (the default; stream_decode.cuh): no producer
 //    warps.  Each of the 4 warps of a CTA (6 at d = 64) takes one contiguous
 //    share of every segment and streams it with 16-byte cp.async copies
 //    (evict-first L2 policy) into a private ring of 3 stages (2 at d = 64

@@ -750,7 +750,9 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
 //   * 32 keys at a time, the next 32 being read meanwhile: 1590 us;
 //   * two threads a row, each half of the keys (16 softmax warps, one read of S a
 //     stage, at 96 registers): 1412 us when this kernel took 1433; the reads of S
-//     take longer the more warps read.
+//     take longer the more warps read;
+//   * the units of the last, part-empty wave split over their keys and merged:
+//     1431 us (8 x 20K with 512 tokens each, 3.4 waves: 1305 for 1357).
 namespace two {
 constexpr int kTiles = 2;
 constexpr int kKWarp0 = 8, kVWarp0 = 12;   // warps 8-11 convert K, 12-15 V

@@ -322,3 +322,64 @@ def test_rescaled_rows_of_a_long_chunk(hq, hkv, d, n, window):
         q = randn((n, hq, d), 5).abs()
         out = f64(run_prefill(c, q.cuda(), starts, n, d ** -0.5, window))
         check_rows(out, c, 0, f64(q), list(range(900 - n, 900)), d ** -0.5, window, True, (d, n))
+
+
+@pytest.mark.parametrize("hq,hkv,d,lens,counts,window", [
+    (32, 8, 128, [900, 300, 257, 1500, 700], [300, 0, 257, 64, 460], 200),      # pairs of tiles: 20 of 8 heads
+    (16, 8, 128, [300 + 7 * i for i in range(40)], [i % 9 for i in range(40)], 0),   # short chunks, some of no row
+    (2, 1, 128, [300] * 153, [1] * 153, 0),
+])
+def test_prefill_of_more_units_than_a_wave(hq, hkv, d, lens, counts, window):
+    c = Cache(hkv, d, lens, seed=len(lens)).cuda()
+    _prefill_case(c, hq, counts, d ** -0.5, window, 3)
+
+
+def test_lengths_out_of_bounds_are_reported_and_leave_the_others():
+    hq, hkv, d = 32, 8, 128
+    c = Cache(hkv, d, [300, 250, 200], seed=1).cuda()
+    counts = (200, 150, 100)
+    q = randn((450, hq, d), 2)
+    starts = torch.tensor([0, 200, 350, 450], dtype=torch.int32).cuda()
+    for bad, length in ((0, 301), (1, 149), (2, -1)):       # past the bound, fewer keys than new tokens, negative
+        ws = fk.alloc_prefill_workspace(3, 200, 300, hq, hkv, d)
+        lens = [300, 250, 200]
+        lens[bad] = length
+        c.gl.copy_(torch.tensor(lens, dtype=torch.int32))
+        out = f64(run_prefill(c, q.cuda(), starts, 200, 0.1, max_len=300, ws=ws))
+        assert fk.fp8kv_read_error(ws) == 1
+        for b, n in enumerate(counts):
+            if b != bad:
+                L = c.lens[b]
+                rows = slice(int(starts[b]), int(starts[b + 1]))
+                check_rows(out[rows], c, b, f64(q[rows]), list(range(L - n, L)), 0.1, 0, True, (bad, b))
+
+
+def test_one_workspace_shared_by_captured_calls_of_different_shapes():
+    """Calls of different shapes that share one workspace, captured into one graph and replayed."""
+    hq, hkv, d = 32, 8, 128
+    c = Cache(hkv, d, [700, 600], seed=5).cuda()
+    qa, qb = randn((1100, hq, d), 1), randn((700, hq, d), 2)
+    sa, sb = (torch.tensor(x, dtype=torch.int32).cuda() for x in ([0, 600, 1100], [0, 300, 700]))
+    ws = fk.alloc_prefill_workspace(2, 600, 700, hq, hkv, d)
+    outs = [torch.zeros_like(x).cuda() for x in (qa, qb)]
+    ga, gb = qa.cuda(), qb.cuda()
+
+    def call():
+        run_prefill(c, ga, sa, 600, 0.1, ws=ws, out=outs[0])
+        run_prefill(c, gb, sb, 400, 0.1, ws=ws, out=outs[1])
+    call()
+    torch.cuda.synchronize()
+    want = [x.clone() for x in outs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(3):
+        for x in outs:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(outs, want))
+    out = f64(outs[1])
+    check_rows(out[:300], c, 0, f64(qb[:300]), list(range(400, 700)), 0.1, 0, True)
+    check_rows(out[300:], c, 1, f64(qb[300:]), list(range(200, 600)), 0.1, 0, True)
+    assert fk.fp8kv_read_error(ws) == 0
