@@ -447,9 +447,13 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
                 // holds: the scores are read once and no maximum is looked for.
                 // A row's first keys, or a page whose weights sum to more than
                 // 2^8 (no weight of a smaller sum is above it, so all are f16),
-                // send the warp the long way.
+                // send the warp the long way.  A look for first keys leaves the
+                // other rows of the warp under their references (a window's
+                // rows start in different stages), so it is followed by the
+                // same question; a look at a pass's sums settles every row.
                 const int k0 = t0 + part * KP, k1 = min(sp1 * kBS, k0 + KP) - 1;
                 bool look = __any_sync(0xffffffffu, m == -INFINITY && rv && pq >= k0 && lq <= k1 && k0 <= k1);
+                bool settled = false;
 #pragma unroll 1
                 while (true) {
                     if (look) {
@@ -503,8 +507,8 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
                         if constexpr (NH > 1) load(st, h);
                         weigh_keys<HK>(sv, scale + HK / kBS * h, cs, m, pcol + HK / 2 * h, ls, top);
                     }
-                    if (look) break;
-                    look = __any_sync(0xffffffffu, top > kMaxSum);
+                    if (settled) break;
+                    look = settled = __any_sync(0xffffffffu, top > kMaxSum);
                     if (!look) break;
                 }
                 if (!ok) break;
