@@ -940,9 +940,10 @@ __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(con
                     float ls, top = 0.f;
                     // as in the one-tile kernel: under the reference the row has,
                     // or the long way for its first keys (looked for in the whole
-                    // stage, at its first half) and for a page that outgrows it
+                    // stage, at its first half) and then for a page that outgrows it
                     bool look = hf == 0 && __any_sync(0xffffffffu, m == -INFINITY && pq >= t0 &&
                                                                        lq < min(t0 + KEYS, sp1 * kBS));
+                    bool settled = false;
 #pragma unroll 1
                     while (true) {
                         if (look) {
@@ -1000,8 +1001,8 @@ __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(con
                         }
                         ls = top = 0.f;
                         weigh_keys<HK>(sv, scale, cs, m, trow + HK / 2 * hf, ls, top);
-                        if (look) break;
-                        look = __any_sync(0xffffffffu, top > kMaxSum);
+                        if (settled) break;
+                        look = settled = __any_sync(0xffffffffu, top > kMaxSum);
                         if (!look) break;
                     }
                     lst += ls;

@@ -47,3 +47,10 @@ def _check(hq, hkv, d, n, by):
 ])
 def test_windows_that_start_in_two_stages_of_a_short_chunk(hq, hkv, d, n, by):
     _check(hq, hkv, d, n, by)
+
+
+@pytest.mark.parametrize("by", ["scores", "value scales"])
+@pytest.mark.parametrize("hq,hkv,d,n", [(1, 1, 128, 512), (2, 1, 128, 200), (2, 2, 128, 129), (1, 1, 64, 512),
+                                        (2, 1, 64, 200), (4, 2, 64, 90)])
+def test_windows_that_start_in_two_stages_of_a_long_chunk(hq, hkv, d, n, by):
+    _check(hq, hkv, d, n, by)
