@@ -263,14 +263,14 @@ __device__ __forceinline__ void simt_consumers(const DecodeArgs& a, const CtaVie
             const uint16_t* src = a.q + (static_cast<int64_t>(w.b) * a.num_q_heads + w.hk * G + j) * D + lane * DPL;
             float x[DPL];
             if constexpr (DPL == 2) {
-                const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(src));
+                const uint32_t u = ld_input(reinterpret_cast<const uint32_t*>(src));
                 x[0] = bf16_to_f32(u & 0xFFFF); x[1] = bf16_to_f32(u >> 16);
             } else if constexpr (DPL == 4) {
-                const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
+                const uint2 u = ld_input(reinterpret_cast<const uint2*>(src));
                 x[0] = bf16_to_f32(u.x & 0xFFFF); x[1] = bf16_to_f32(u.x >> 16);
                 x[2] = bf16_to_f32(u.y & 0xFFFF); x[3] = bf16_to_f32(u.y >> 16);
             } else {
-                const uint4 u = __ldg(reinterpret_cast<const uint4*>(src));
+                const uint4 u = ld_input(reinterpret_cast<const uint4*>(src));
                 const uint32_t ww[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) { x[2 * i] = bf16_to_f32(ww[i] & 0xFFFF); x[2 * i + 1] = bf16_to_f32(ww[i] >> 16); }
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const int b = b0 + lane;
             int n = 0;
             if (b < B) {
-                const int Lraw = __ldg(a.seq_lens + b);
+                const int Lraw = ld_input(a.seq_lens + b);
                 if (Lraw < 0 || Lraw > a.max_seq_len) report(a.err, FP8KV_ERR_INVALID_ARG);
                 lens[b] = clamp_len(Lraw, a.max_seq_len);
                 n = attended_pages(lens[b], a.window);
@@ -689,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     // with two units per cache head both write the same bytes: identical values
                     uint8_t* dst_row = cache + ((static_cast<int64_t>(id) * Hc + (hk >> kvs)) * kBS + (L - 1) % kBS) * D;
                     store_new_row<D>(batch_row, dst_row, lane,
-                                           head_scales ? __ldg(head_scales + (hk >> kvs)) : scale_raw);
+                                           head_scales ? ld_input(head_scales + (hk >> kvs)) : scale_raw);
                     fence_proxy_async_global();
                 }
                 __syncwarp();

@@ -100,7 +100,7 @@ __device__ __forceinline__ void load_stage_tc(const Args& a, const int32_t* bt, 
     constexpr int kChunks = kBS * Tg::CPR;      // 16-byte chunks per page
     for (int i = tid; i < np * kChunks; i += 128) {
         const int p = i / kChunks, ci = i % kChunks;
-        int id = __ldg(bt + pg + p);
+        int id = ld_input(bt + pg + p);
         if (id < 0 || id >= a.num_blocks) {
             if (ci == 0) report(a.err, FP8KV_ERR_INVALID_ARG);
             id = 0;
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(128) paged_prefill_tc_kernel(const Args a) {
         for (int ps = 0; ps < NP; ++ps)
 #pragma unroll
             for (int c = 0; c < PC; ++c) {
-                qv[c] = rv ? __ldg(qrow + ps * PC + c) : make_uint4(0, 0, 0, 0);
+                qv[c] = rv ? ld_input(qrow + ps * PC + c) : make_uint4(0, 0, 0, 0);
                 const uint32_t w4[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(128) paged_prefill_tc_kernel(const Args a) {
 #pragma unroll
             for (int cc = 0; cc < PC; ++cc) {
                 const int c = ps * PC + cc;
-                if (NP > 1) qv[cc] = rv ? __ldg(qrow + c) : make_uint4(0, 0, 0, 0);
+                if (NP > 1) qv[cc] = rv ? ld_input(qrow + c) : make_uint4(0, 0, 0, 0);
                 const uint32_t w4[4] = {qv[cc].x, qv[cc].y, qv[cc].z, qv[cc].w};
                 uint32_t f[4];
 #pragma unroll
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(ws::kThreads, 1) paged_prefill_ws_kernel(const
         float qmax = 0.f;
 #pragma unroll 4
         for (int c = 0; c < NC; ++c) {
-            const uint4 qv = rv ? __ldg(qrow + c) : make_uint4(0, 0, 0, 0);
+            const uint4 qv = rv ? ld_input(qrow + c) : make_uint4(0, 0, 0, 0);
             const uint32_t w4[4] = {qv.x, qv.y, qv.z, qv.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(ws::kThreads, 1) paged_prefill_ws_kernel(const
         const float up = (a.score_scale < 0.f ? -1.f : 1.f) * __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
 #pragma unroll 4
         for (int c = 0; c < NC; ++c) {
-            const uint4 qv = rv ? __ldg(qrow + c) : make_uint4(0, 0, 0, 0);
+            const uint4 qv = rv ? ld_input(qrow + c) : make_uint4(0, 0, 0, 0);
             const uint32_t w4[4] = {qv.x, qv.y, qv.z, qv.w};
             uint32_t f[4];
 #pragma unroll
@@ -948,7 +948,7 @@ __global__ void __launch_bounds__(ws1::kThreads, Ws1Geo<D>::kCtasPerSm) paged_pr
         float qmax = 0.f;
 #pragma unroll 4
         for (int c = 0; c < NC; ++c) {
-            const uint4 qv = rv ? __ldg(qrow + c) : make_uint4(0, 0, 0, 0);
+            const uint4 qv = rv ? ld_input(qrow + c) : make_uint4(0, 0, 0, 0);
             const uint32_t w4[4] = {qv.x, qv.y, qv.z, qv.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -964,7 +964,7 @@ __global__ void __launch_bounds__(ws1::kThreads, Ws1Geo<D>::kCtasPerSm) paged_pr
         const float up = (a.score_scale < 0.f ? -1.f : 1.f) * __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
 #pragma unroll 4
         for (int c = 0; c < NC; ++c) {
-            const uint4 qv = rv ? __ldg(qrow + c) : make_uint4(0, 0, 0, 0);
+            const uint4 qv = rv ? ld_input(qrow + c) : make_uint4(0, 0, 0, 0);
             const uint32_t w4[4] = {qv.x, qv.y, qv.z, qv.w};
             uint32_t f[4];
 #pragma unroll

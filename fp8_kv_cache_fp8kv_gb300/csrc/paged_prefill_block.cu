@@ -42,7 +42,7 @@ struct PageScales {
 
     // The id as the table has it: looking at it here would wait for the read.
     __device__ __forceinline__ int block_of(int pg) const {
-        return lane < PAGES && pg + lane < end ? __ldg(bt + pg + lane) : 0;
+        return lane < PAGES && pg + lane < end ? ld_input(bt + pg + lane) : 0;
     }
     // The scales of the pages at pg, whose ids are held; 1 past the range.  A
     // bad id reads block 0's, as the copies do (they report it).
@@ -50,8 +50,8 @@ struct PageScales {
         k = v = 1.f;
         if (lane < PAGES && pg + lane < end) {
             const int64_t b = id >= 0 && id < a.num_blocks ? id : 0;
-            k = __ldg(a.k_page_scales + b * a.num_kv_heads + hk);
-            v = __ldg(a.v_page_scales + b * a.num_kv_heads + hk);
+            k = ld_input(a.k_page_scales + b * a.num_kv_heads + hk);
+            v = ld_input(a.v_page_scales + b * a.num_kv_heads + hk);
         }
     }
     // Starts the reads of the stage at page pg and of the block ids after it.
@@ -97,7 +97,7 @@ __device__ __forceinline__ void build_q_tiles(const Args& a, const Unit& u, int 
         const int row = row_of(i), rr = R0 + row;
         qv[i] = make_uint4(0, 0, 0, 0);
         if (row < ROWS && rr < u.rows)
-            qv[i] = __ldg(reinterpret_cast<const uint4*>(
+            qv[i] = ld_input(reinterpret_cast<const uint4*>(
                         a.q + (static_cast<int64_t>(u.q0 + (rr >> lg)) * a.num_q_heads + (hk << lg) +
                                (rr & ((1 << lg) - 1))) * D) + c);
     }
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
     // at it here would wait for the read).
     auto blocks_of = [&](int s) {
         const int pg = sp0 + s * PAGES + lane;
-        return lane < PAGES && pg < sp1 ? __ldg(bt + pg) : 0;
+        return lane < PAGES && pg < sp1 ? ld_input(bt + pg) : 0;
     };
     // A copy warp's half of stage s (K rows or V rows) into its ring slot; the
     // slot's barrier counts the copies as they land.
@@ -847,7 +847,7 @@ __global__ void __launch_bounds__(two::kThreads, 1) paged_prefill_two_kernel(con
     // at it here would wait for the read).
     auto blocks_of = [&](int s) {
         const int pg = sp0 + s * PAGES + lane;
-        return lane < PAGES && pg < sp1 ? __ldg(bt + pg) : 0;
+        return lane < PAGES && pg < sp1 ? ld_input(bt + pg) : 0;
     };
     auto copy_stage = [&](int s, int ids) {       // one commit group per stage, also an empty one
         const int np = sp1 - sp0 - s * PAGES;     // pages left (<= 0 past the range)

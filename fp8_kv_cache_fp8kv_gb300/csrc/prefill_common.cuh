@@ -97,10 +97,10 @@ __device__ __forceinline__ bool make_unit(const Args& a, int b, int tile, bool r
         if constexpr (G > 0) return r / G;
         else return r >> a.log2_group;
     };
-    u.q0 = __ldg(a.q_starts + b);
-    const int L_in = __ldg(a.seq_lens + b);
+    u.q0 = ld_input(a.q_starts + b);
+    const int L_in = ld_input(a.seq_lens + b);
     u.L = L_in < 0 ? 0 : min(L_in, a.max_seq_len);
-    const int n_in = __ldg(a.q_starts + b + 1) - u.q0;
+    const int n_in = ld_input(a.q_starts + b + 1) - u.q0;
     int n = n_in < 0 ? 0 : min(n_in, min(u.L, a.max_q_len));
     if (u.q0 < 0 || u.q0 + static_cast<int64_t>(n) > a.num_q_tokens) n = 0;  // never touch rows outside q / out
     if (report_errors && (u.L != L_in || n != n_in)) report(a.err, FP8KV_ERR_INVALID_ARG);

@@ -73,6 +73,18 @@ __device__ __forceinline__ void griddep_launch_dependents() {
 // operations are visible.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Reads a value that the caller, or an earlier kernel of this library, has
+// written: an ordinary load.  A grid launched programmatically is resident
+// while the grid before it may still write (the appends write the queries and
+// page scales that attention reads), and a read-only load (__ldg, or what the
+// compiler makes of a const __restrict__ pointer) is defined only for data that
+// does not change while the kernel is there; griddep_wait makes the writes
+// visible to ordinary loads.
+template <typename T>
+__device__ __forceinline__ T ld_input(const T* p) {
+    return *p;
+}
+
 // ---------------------------------------------------------------- TMA
 
 // 4-D tiled tensor load into shared memory, completing on `bar` (tx bytes).

@@ -29,10 +29,10 @@ namespace fp8kv {
 
 template <bool E5M2>
 __global__ void __launch_bounds__(256) quant_append_kernel(
-    const uint4* __restrict__ k_new, const uint4* __restrict__ v_new, const int64_t* __restrict__ slot_mapping,
+    const uint4* k_new, const uint4* v_new, const int64_t* slot_mapping,
     int64_t num_tokens, uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache, int64_t num_slots,
     int num_kv_heads, int head_dim, int block_size, float k_scale, float v_scale,
-    const float* __restrict__ k_scales, const float* __restrict__ v_scales) {
+    const float* k_scales, const float* v_scales) {
     // A decode launched right after may get resident now (it waits for this
     // grid before reading anything).
     griddep_launch_dependents();
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(256) quant_append_kernel(
         const int64_t rem = j - t * chunks_per_token;
         const int64_t hk = rem / chunks_per_row;
         const int64_t c = rem - hk * chunks_per_row;
-        const int64_t slot = __ldg(slot_mapping + t);
+        const int64_t slot = ld_input(slot_mapping + t);
         if (slot < 0 || slot >= num_slots) continue;
         const int64_t blk = slot / block_size;
         const int64_t off = slot - blk * block_size;
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(256) quant_append_kernel(
         const uint4 b = __ldcs(src + 1);
         // per-tensor scale, or the kv head's own one ([Hkv] arrays)
         const float* hs = is_v ? v_scales : k_scales;
-        const float s = hs ? __ldg(hs + hk) : (is_v ? v_scale : k_scale);
+        const float s = hs ? ld_input(hs + hk) : (is_v ? v_scale : k_scale);
         const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         uint32_t o[4];
 #pragma unroll

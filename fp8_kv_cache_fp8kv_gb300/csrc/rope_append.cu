@@ -124,9 +124,9 @@ __device__ __forceinline__ void fill_table(float4* tab, const Rope& rp, int64_t 
             if (rp.positions) {
                 int ax = rp.freq_axis ? rp.freq_axis[f0 + e] : 0;
                 ax = ax < rp.axes ? ax : 0;                 // never past the positions array
-                pos = __ldg(rp.positions + static_cast<int64_t>(ax) * num_tokens + t0 + tok);
+                pos = ld_input(rp.positions + static_cast<int64_t>(ax) * num_tokens + t0 + tok);
             }
-            cs[e] = turn_sincos(pos, __ldg(rp.inv_freq + f0 + e));
+            cs[e] = turn_sincos(pos, ld_input(rp.inv_freq + f0 + e));
         }
         tab[i] = make_float4(cs[0].x, cs[0].y, cs[1].x, cs[1].y);
     }
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const SlotArgs a)
     auto ready = [&]() {          // the rotation table and the slots
         fill_table(tab, a.rp, t0, cnt, 0, rw.num_tokens, tid);
         if (tid < cnt) {
-            const int64_t s = __ldg(a.slots + t0 + tid), blk = s / a.block_size;
+            const int64_t s = ld_input(a.slots + t0 + tid), blk = s / a.block_size;
             row_sh[tid] = s >= 0 && s < a.num_slots ? blk * rw.hkv * a.block_size + (s - blk * a.block_size) : -1;
         }
         __syncthreads();
@@ -341,10 +341,10 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const SlotArgs a)
         } else {
             constexpr bool E5M2 = FMT == FP8KV_CACHE_E5M2;
             uint32_t o[4];
-            codes16<E5M2>(x, a.k_scales ? __ldg(a.k_scales + h) : a.k_scale, o);
+            codes16<E5M2>(x, a.k_scales ? ld_input(a.k_scales + h) : a.k_scale, o);
             store_codes(static_cast<uint8_t*>(a.k_cache) + row, e0, e1, o);
             unpack(v0, v1, x);
-            codes16<E5M2>(x, a.v_scales ? __ldg(a.v_scales + h) : a.v_scale, o);
+            codes16<E5M2>(x, a.v_scales ? ld_input(a.v_scales + h) : a.v_scale, o);
             *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.v_cache) + row + 16 * j) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
@@ -466,28 +466,28 @@ __device__ __forceinline__ PageWork find_page(const BlockArgs& a, int lane) {
         int own0 = 0, own1 = 0, own_len = 0;
         const bool own = x < a.batch;
         if (own) {
-            own0 = __ldg(a.q_starts + x);
-            own1 = __ldg(a.q_starts + x + 1);
-            own_len = __ldg(a.seq_lens + x);
+            own0 = ld_input(a.q_starts + x);
+            own1 = ld_input(a.q_starts + x + 1);
+            own_len = ld_input(a.seq_lens + x);
         }
         int lo = 0, cnt = a.batch;
         while (cnt > 1) {
             const int step = (cnt + 31) / 32;
             const int at = lo + lane * step;
             const bool le = lane * step < cnt &&
-                            static_cast<int64_t>(__ldg(a.q_starts + at)) / kBS + 2 * static_cast<int64_t>(at) <= x;
+                            static_cast<int64_t>(ld_input(a.q_starts + at)) / kBS + 2 * static_cast<int64_t>(at) <= x;
             const int k = max(1, __popc(__ballot_sync(0xffffffffu, le)));
             const int skip = (k - 1) * step;
             lo += skip;
             cnt = min(step, cnt - skip);
         }
         b = lo;
-        q0 = __ldg(a.q_starts + b);
-        n = __ldg(a.q_starts + b + 1) - q0;
+        q0 = ld_input(a.q_starts + b);
+        n = ld_input(a.q_starts + b + 1) - q0;
         j = x - (q0 / kBS + 2 * static_cast<int64_t>(b));
         if (own && own0 != own1 && !fits(own0, static_cast<int64_t>(own1) - own0, own_len)) report();
     }
-    const int L = __ldg(a.seq_lens + b);
+    const int L = ld_input(a.seq_lens + b);
     if (!a.q_starts && L == 0) return w;    // an empty slot of a padded batch
     if (n == 0) return w;
     if (!fits(q0, n, L)) {
@@ -503,7 +503,7 @@ __device__ __forceinline__ PageWork find_page(const BlockArgs& a, int lane) {
     w.cnt = min(L - first, kBS) - w.r0;
     w.pos = start;
     w.t0 = q0 + (start - p0);
-    w.block = __ldg(a.block_tables + static_cast<int64_t>(b) * a.max_blocks_per_seq + page);
+    w.block = ld_input(a.block_tables + static_cast<int64_t>(b) * a.max_blocks_per_seq + page);
     if (w.block < 0 || w.block >= a.num_blocks) {
         report();
         w.block = -1;

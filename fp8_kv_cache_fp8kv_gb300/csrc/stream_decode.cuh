@@ -166,7 +166,7 @@ __device__ __forceinline__ int load_block_id(const int32_t* row, int lane, int c
                                              uint32_t* err) {
     int id = 0;
     if (lane < count) {
-        id = __ldg(row + lane);
+        id = ld_input(row + lane);
         if (id < 0 || id >= num_blocks) {
             report(err, FP8KV_ERR_INVALID_ARG);
             id = -1;
@@ -186,7 +186,7 @@ template <int D>
 __device__ __forceinline__ void load_new_row(NewRow<D>& r, const uint16_t* src_row, int lane) {
     const uint32_t* p = reinterpret_cast<const uint32_t*>(src_row + lane * (D / 32));
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) r.w[i] = __ldg(p + i);
+    for (int i = 0; i < D / 64; ++i) r.w[i] = ld_input(p + i);
 }
 
 // Quantise-on-append of the warp's row: code = E4M3_satfinite(fp32(x) / scale)
@@ -230,11 +230,11 @@ __device__ __forceinline__ void codes4_to_f16x2x2(uint32_t w, uint32_t& lo, uint
 // Score multiplier (sm_scale * k_scale * log2 e, multiplied in that order as
 // the host does for the per-tensor scale) and V scale of kv head hk.
 __device__ __forceinline__ float unit_score_scale(const DecodeArgs& a, int hk) {
-    return a.k_scales ? (a.sm_scale * __ldg(a.k_scales + (hk >> a.kv_shift))) * kLog2e : a.score_scale;
+    return a.k_scales ? (a.sm_scale * ld_input(a.k_scales + (hk >> a.kv_shift))) * kLog2e : a.score_scale;
 }
 
 __device__ __forceinline__ float unit_v_scale(const DecodeArgs& a, int hk) {
-    return a.v_scales ? __ldg(a.v_scales + (hk >> a.kv_shift)) : a.v_scale;
+    return a.v_scales ? ld_input(a.v_scales + (hk >> a.kv_shift)) : a.v_scale;
 }
 
 template <int D, int G>
@@ -249,7 +249,7 @@ __device__ __forceinline__ void load_query(const DecodeArgs& a, int b, int hk, i
         for (int c = 0; c < Gm::KW / 8; ++c) {
             uint4 v = make_uint4(0, 0, 0, 0);
             if (h0 + gid < G)
-                v = __ldg(reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(b) * a.num_q_heads + hk * G + h0 + gid) * D +
+                v = ld_input(reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(b) * a.num_q_heads + hk * G + h0 + gid) * D +
                                                          hh * 128 + tig * Gm::KW) + c);
             const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -297,8 +297,8 @@ __device__ __forceinline__ void load_query_bf16(const DecodeArgs& a, int b, int 
         if (h0 + gid < G) {
             const uint4* src = reinterpret_cast<const uint4*>(
                 a.q + (static_cast<int64_t>(b) * a.num_q_heads + hk * G + h0 + gid) * D + hh * Gm::DBOX + tig * 16);
-            v0 = __ldg(src);
-            v1 = __ldg(src + 1);
+            v0 = ld_input(src);
+            v1 = ld_input(src + 1);
         }
         const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(StreamCfg<D, ES, G>::NW * 32, kCtasPerSm)
             const int b = b0 + lane;
             int n = 0;
             if (b < B) {
-                const int Lraw = __ldg(a.seq_lens + b);
+                const int Lraw = ld_input(a.seq_lens + b);
                 if (Lraw < 0 || Lraw > a.max_seq_len) report(a.err, FP8KV_ERR_INVALID_ARG);
                 lens[b] = clamp_len(Lraw, a.max_seq_len);
                 n = attended_pages(lens[b], a.window);
@@ -894,8 +894,8 @@ __global__ void __launch_bounds__(StreamCfg<D, ES, G>::NW * 32, kCtasPerSm)
                     // append kernel), then copy it
                     const int L = lens[cur.pos.w.b];
                     const int64_t roff = static_cast<int64_t>((L - 1) % kBS) * D;
-                    const float ksc = a.k_scales ? __ldg(a.k_scales + (cur.pos.w.hk >> kvs)) : a.k_scale_raw;
-                    const float vsc = a.v_scales ? __ldg(a.v_scales + (cur.pos.w.hk >> kvs)) : a.v_scale_raw;
+                    const float ksc = a.k_scales ? ld_input(a.k_scales + (cur.pos.w.hk >> kvs)) : a.k_scale_raw;
+                    const float vsc = a.v_scales ? ld_input(a.v_scales + (cur.pos.w.hk >> kvs)) : a.v_scale_raw;
                     store_new_row<D, E5M2>(cur.krow, a.k_cache + page * Gm::PAGE + roff, lane, ksc);
                     store_new_row<D, E5M2>(cur.vrow, a.v_cache + page * Gm::PAGE + roff, lane, vsc);
                     __threadfence();
@@ -1089,7 +1089,7 @@ __global__ void __launch_bounds__(merge_threads<D>()) merge_kernel(const DecodeA
     const int Hkv = a.num_kv_heads, b = u / Hkv, hk = u - b * Hkv;
     long long before = 0, total = 0;
     for (int i = tid; i < a.batch; i += kMergeThreads) {
-        const int n = attended_pages(clamp_len(__ldg(a.seq_lens + i), a.max_seq_len), a.window);
+        const int n = attended_pages(clamp_len(ld_input(a.seq_lens + i), a.max_seq_len), a.window);
         total += n;
         before += i < b ? n : 0;
     }
@@ -1109,7 +1109,7 @@ __global__ void __launch_bounds__(merge_threads<D>()) merge_kernel(const DecodeA
         before += red[0][w];
         total += red[1][w];
     }
-    const int nb = attended_pages(clamp_len(__ldg(a.seq_lens + b), a.max_seq_len), a.window);
+    const int nb = attended_pages(clamp_len(ld_input(a.seq_lens + b), a.max_seq_len), a.window);
     int k_u = 0, c_first = 0;
     if (nb > 0) {
         const int64_t P = static_cast<int64_t>(Hkv) * total;
