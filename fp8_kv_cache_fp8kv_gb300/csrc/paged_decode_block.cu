@@ -4,17 +4,18 @@
 // Accuracy Risk", "Scales and calibration".
 //
 // The kernel is stream_decode_kernel (stream_decode.cuh) with BS = true.  With
-// c_t the codes and ks, vs the scales of key t's page,
-//     s_t = sm (q . ck_t) ks,   out = sum_t p_t vs cv_t / sum_t p_t,
-// so the scales cost one multiplication per score (folded into the score
-// multiplier) and one per element of a page's P.V tile.  They are read from
+// c_t the codes and ks, vs the scales of key t's page, in log2 units,
+//     s_t = sm (q . ck_t) ks,   w_t = 2^(s_t + log2 vs - m),
+//     out = sum_t w_t cv_t / sum_t (w_t / vs),
+// m the largest s_t + log2 vs: the scales are the multiplier and the addend of
+// one FMA a score, and the row sum takes a factor a page.  They are read from
 // HBM with the pages: 8 bytes beside a page's 32 d bytes, as 4-byte cp.async
 // copies in the stage's own group.
 //
 // What bounds it is what bounds the kernel without them (stream_decode.cuh): HBM
-// and the fixed cost of a step.  8 x 20K, 32 over 8 heads, d = 128: 61.3 us, 329 MB
-// at 5.4 TB/s (61.8 with one scale per tensor and the append fused in); 1 x 128K,
-// 64 over 8 heads: 49.9 us, 5.4 TB/s; 1 x 4096: 9.3 us; 9 sequences behind a window
+// and the fixed cost of a step.  8 x 20K, 32 over 8 heads, d = 128: 62.2 us, 329 MB
+// at 5.3 TB/s (59.5 with one scale per tensor and the append fused in); 1 x 128K,
+// 64 over 8 heads: 50.4 us, 5.3 TB/s; 1 x 4096: 9.4 us; 9 sequences behind a window
 // of 128: 13.4 us.
 #include "stream_decode.cuh"
 

@@ -221,6 +221,20 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+// log2 x within 2 ulp, for normal x.
+__device__ __forceinline__ float fast_log2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1 / x within 1 ulp, for normal x (exact for powers of two).
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // ---------------------------------------------------------------- CUDA-core FP32 accumulation
 
 // acc_lo += a.lo * b.lo, acc_hi += a.hi * b.hi for f16x2 words a, b: the

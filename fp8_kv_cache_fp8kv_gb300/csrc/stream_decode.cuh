@@ -405,11 +405,22 @@ __device__ __forceinline__ void absorb(const float* x, int lane, float (&m)[2], 
 // the running state (m, l, o) of the warp.  The query heads sit on the MMA's
 // n side, 8 per n-tile: NT = 2 n-tiles carry g = 16 heads, and the converted
 // K and V fragments feed both tiles' MMAs, so each page is read once.
-// BS: page p's scores are multiplied by its K scale psc[p].x, and its P.V tile
-// goes into fresh accumulators and is multiplied by its V scale psc[p].y as it
-// is folded in (IEEE FMA).  Weighing P by the V scale instead would save the
-// multiplications, but P is f16 there: beside a page of a 2^20 times larger
-// scale, a page that carries all the probability would keep 4 bits of it.
+// BS: with ks, vs = psc[p] the scales of page p, a key's weight is
+// w = 2^(s ks + log2 vs - m), so the V scale costs an addend of the score's FMA;
+// the row sum takes w / vs, and out = o / l.  m is the largest s ks + log2 vs
+// less kRoom, rounded up so that no weight passes 2^15 (f16 ends at 65504) at
+// any size of the scores.  P is the f16 of w: what it rounds is relative to the
+// largest p vs, as the answer is; 2^-29 of that still has 11 bits, and below
+// 2^-40 of it nothing is left.  (Relative to the largest p, with the page's P.V
+// tile multiplied by vs, a page of 2^26 times the others' V scale and 2^-26 of
+// their probability, half the answer, was lost.)
+// Measured against a factor per page in FP32 (the page's V scale times
+// 2^(page maximum - m), P relative to the page): 8 x 20K, d = 128, g = 4: 62.2 us
+// both; 8 x 16K, d = 64, g = 8: 32.4 and 34.8; 4 x 32K, d = 128, g = 16: 69.1 and
+// 70.3; 8 x 8K, d = 256: 20.7 and 20.2.  The kernel that lost such pages took 61.7,
+// 32.4, 65.7 and 19.9 (g = 16 at d = 128 now has 255 registers and spills 16 bytes).
+constexpr float kRoom = 15.f;
+
 template <int D, int ES, bool E5M2, int NT, bool BS>
 __device__ __forceinline__ void tc_stage(const uint8_t* kst, const uint8_t* vst, const float2* psc, int np,
                                          int tok_base, int lo, int L,
@@ -482,10 +493,15 @@ __device__ __forceinline__ void tc_stage(const uint8_t* kst, const uint8_t* vst,
             for (int r = 0; r < 4; ++r) sc[p][t][r] += s1[t][r];
     }
 
-    float2 ps[BS ? Gm::PPS : 1];
+    float kscale[BS ? Gm::PPS : 1], vlog[BS ? Gm::PPS : 1], vinv[BS ? Gm::PPS : 1];
     if constexpr (BS) {
 #pragma unroll
-        for (int p = 0; p < Gm::PPS; ++p) ps[p] = p < np ? psc[p] : make_float2(0.f, 0.f);
+        for (int p = 0; p < Gm::PPS; ++p) {
+            const float2 ps = p < np ? psc[p] : make_float2(1.f, 1.f);
+            kscale[p] = ps.x;
+            vlog[p] = fast_log2(ps.y);
+            vinv[p] = fast_rcp(ps.y);
+        }
     }
 
     // ---- mask, scale to log2 units, stage maximum
@@ -502,8 +518,8 @@ __device__ __forceinline__ void tc_stage(const uint8_t* kst, const uint8_t* vst,
                 const bool valid = interior || ((p < np) && tok >= lo && tok < L);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float c = BS ? cs[t][j] * ps[p].x : cs[t][j];
-                    const float x = valid ? sc[p][t][2 * e2 + j] * c : -INFINITY;
+                    const float raw = sc[p][t][2 * e2 + j];
+                    const float x = !valid ? -INFINITY : BS ? fmaf(raw, cs[t][j] * kscale[p], vlog[p]) : raw * cs[t][j];
                     sc[p][t][2 * e2 + j] = x;
                     mx[t][j] = fmaxf(mx[t][j], x);
                 }
@@ -517,7 +533,7 @@ __device__ __forceinline__ void tc_stage(const uint8_t* kst, const uint8_t* vst,
             mx[t][j] = fmaxf(mx[t][j], __shfl_xor_sync(0xffffffffu, mx[t][j], 4));
             mx[t][j] = fmaxf(mx[t][j], __shfl_xor_sync(0xffffffffu, mx[t][j], 8));
             mx[t][j] = fmaxf(mx[t][j], __shfl_xor_sync(0xffffffffu, mx[t][j], 16));
-            const float mn = fmaxf(m[t][j], mx[t][j]);
+            const float mn = fmaxf(m[t][j], BS ? __fadd_ru(mx[t][j], -kRoom) : mx[t][j]);
             muse[t][j] = mn == -INFINITY ? 0.f : mn;
             alpha[t][j] = fast_exp2(m[t][j] - muse[t][j]);
             m[t][j] = mn;
@@ -534,8 +550,13 @@ __device__ __forceinline__ void tc_stage(const uint8_t* kst, const uint8_t* vst,
             const float p01 = fast_exp2(sc[p][t][1] - muse[t][1]);
             const float p10 = fast_exp2(sc[p][t][2] - muse[t][0]);
             const float p11 = fast_exp2(sc[p][t][3] - muse[t][1]);
-            lsum[0] += p00 + p10;
-            lsum[1] += p01 + p11;
+            if constexpr (BS) {
+                lsum[0] = fmaf(p00 + p10, vinv[p], lsum[0]);
+                lsum[1] = fmaf(p01 + p11, vinv[p], lsum[1]);
+            } else {
+                lsum[0] += p00 + p10;
+                lsum[1] += p01 + p11;
+            }
             if constexpr (ES == 1) {
                 pb[p][t][0] = movmatrix_trans(pack_f16x2(p00, p01));
                 pb[p][t][1] = movmatrix_trans(pack_f16x2(p10, p11));
@@ -548,7 +569,7 @@ __device__ __forceinline__ void tc_stage(const uint8_t* kst, const uint8_t* vst,
         l[t][1] = l[t][1] * alpha[t][1] + lsum[1];
     }
 
-    // ---- P.V tile of this stage (BS: of each page): O^T[dim][head] = V^T P^T
+    // ---- P.V tile of this stage: O^T[dim][head] = V^T P^T
     float ot[NT][Gm::MT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -557,15 +578,6 @@ __device__ __forceinline__ void tc_stage(const uint8_t* kst, const uint8_t* vst,
 #pragma unroll
     for (int p = 0; p < Gm::PPS; ++p) {
         if (p < np) {
-            if constexpr (BS) {
-                if (p > 0) {
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int mt = 0; mt < Gm::MT; ++mt)
-                            ot[t][mt][0] = ot[t][mt][1] = ot[t][mt][2] = ot[t][mt][3] = 0.f;
-                }
-            }
 #pragma unroll
             for (int hh = 0; hh < Gm::HALVES; ++hh) {
                 uint32_t v[4][Gm::VW / 4];
@@ -602,30 +614,19 @@ __device__ __forceinline__ void tc_stage(const uint8_t* kst, const uint8_t* vst,
                     }
                 }
             }
-            if constexpr (BS) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int mt = 0; mt < Gm::MT; ++mt)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            o[t][mt][r] = fmaf(ot[t][mt][r], ps[p].y, p == 0 ? o[t][mt][r] * alpha[t][r & 1] : o[t][mt][r]);
-            }
         }
     }
 
     // ---- fold the tile into the FP32 accumulators
-    if constexpr (!BS) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int mt = 0; mt < Gm::MT; ++mt) {
-                o[t][mt][0] = fmaf(o[t][mt][0], alpha[t][0], ot[t][mt][0]);
-                o[t][mt][1] = fmaf(o[t][mt][1], alpha[t][1], ot[t][mt][1]);
-                o[t][mt][2] = fmaf(o[t][mt][2], alpha[t][0], ot[t][mt][2]);
-                o[t][mt][3] = fmaf(o[t][mt][3], alpha[t][1], ot[t][mt][3]);
-            }
-    }
+        for (int mt = 0; mt < Gm::MT; ++mt) {
+            o[t][mt][0] = fmaf(o[t][mt][0], alpha[t][0], ot[t][mt][0]);
+            o[t][mt][1] = fmaf(o[t][mt][1], alpha[t][1], ot[t][mt][1]);
+            o[t][mt][2] = fmaf(o[t][mt][2], alpha[t][0], ot[t][mt][2]);
+            o[t][mt][3] = fmaf(o[t][mt][3], alpha[t][1], ot[t][mt][3]);
+        }
 }
 
 // Combines the k_u partials of unit u (slots u + c_first ...) into its output

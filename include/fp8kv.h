@@ -560,10 +560,12 @@ fp8kv_status fp8kv_rope_append_block(const void* q, int64_t q_stride, void* q_ou
 /*
  * fp8kv_paged_decode over a block-scaled cache: key t's code stands for
  * decode(code) * k_scales[page(t)][hk], value t's for decode(code) *
- * v_scales[page(t)][hk].  Scores are scaled page by page in FP32; each page's
- * P.V tile is multiplied by its V scale as it is added into the FP32
- * accumulators, so pages of very different scales do not cost one another
- * precision.  All other arguments, the workspace
+ * v_scales[page(t)][hk].  Scores are scaled page by page in FP32; a key's weight
+ * is its probability times its page's V scale, rounded to f16 (11 bits) for the
+ * tensor cores: relative to itself where it is at least 2^-29 of the largest
+ * such weight, in steps of 2^-39 of the largest below that.  So a page counts
+ * by what it brings to the answer, whatever its scale and probability are for
+ * themselves.  Sums are FP32.  All other arguments, the workspace
  * (fp8kv_paged_decode_workspace_size) and the errors as fp8kv_paged_decode.
  */
 fp8kv_status fp8kv_paged_decode_block(const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
@@ -575,7 +577,9 @@ fp8kv_status fp8kv_paged_decode_block(const void* q, const uint8_t* k_cache, con
 
 /*
  * fp8kv_paged_prefill over a block-scaled cache (append the chunk first, with
- * fp8kv_rope_append_block).  All other arguments, the workspace
+ * fp8kv_rope_append_block).  Weights are rounded as fp8kv_paged_decode_block's,
+ * with less room: relative to themselves down to 2^-14 of a row's largest, in
+ * steps of 2^-24 of it below.  All other arguments, the workspace
  * (fp8kv_paged_prefill_workspace_size) and the errors as fp8kv_paged_prefill.
  * What a row may not attend does not reach it, with one exception, as in
  * fp8kv_paged_prefill: a NaN code in V makes NaN of its dimension in every
