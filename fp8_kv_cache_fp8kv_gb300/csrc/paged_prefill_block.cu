@@ -1,8 +1,7 @@
 // Chunked-prefill attention over a block-scaled E4M3 cache: one K and one V
 // scale for every (page, kv head), the granularity below the per-tensor and
 // per-head scales of gpusmith.com, "FP8 KV Cache Quantization: Capacity Gains
-// and Accuracy Risk", "Scales and calibration".  How the scales enter the
-// softmax is described at PageScales (prefill_common.cuh).
+// and Accuracy Risk", "Scales and calibration".
 //
 // Two kernels on the 5th-generation tensor cores: chunks of several query tiles
 // at d = 64 and 128 run the two-tile kernel, everything else -- d = 256, and
@@ -18,8 +17,9 @@
 // of the FMA that applies the score multiplier, one multiplier and one addend
 // per page of 16 keys.  m refers to s + log2 vs, so weights stay small however
 // the scales differ, and a weight is rounded to f16 relative to the largest in
-// the sum it enters.  The row sum takes each page's weights times 1 / vs, in
-// FP32.
+// the sum it enters.  The row sum takes each page's weights, unrounded, times
+// 1 / vs, in FP32.  The exponent is one FMA of the raw score, off by up to
+// 2^-23 of m: scores beyond 2^26 in size could leave f16's range.
 #include <cuda_fp16.h>
 
 #include "prefill_common.cuh"
@@ -225,16 +225,19 @@ constexpr float kMaxSum = 256.f;
 // Every mbarrier wait is bounded, and the first role to give up ends the
 // others' waits (abort flag), as in the two-tile kernel.
 //
-// Measured: 8 x 20K, 32 over 8 heads, d = 128, 9 new tokens: 116 us, 330 MB
-// read at 2.85 TB/s (the hand-overs and MMAs alone take 83, of which 27 are the
-// three waves' first stages); 4 x 9K, 777 new tokens, window 512, 8 over 1 heads, d = 256:
-// 42 us, 310 TFLOP/s, two waves of one CTA per SM.  With 2 splits a unit and one
-// wave (128 CTAs) the first took 127.  REP by the rows a chunk may have: 8 x 20K,
-// 8 tokens (32 rows): 99 us with four copies, 112 with two or one; 8 x 16K, d = 64,
-// 4 tokens (32 rows): 70, 82 and 86, 8 tokens (64 rows): 82 with two, 87 with one;
-// d = 256, 16 x 9K, 8 tokens (64 rows): 38 and 40; without difference at 64 rows
-// of d = 128 (114.8).  Against the two-tile kernel, 8 x 20K: 33 tokens (two tiles)
-// 228 us and 186 there.
+// Measured: 8 x 20K, 32 over 8 heads, d = 128, 5 to 14 new tokens: 120 us, 330 MB
+// read at 2.75 TB/s (the hand-overs and MMAs alone take 83, of which 27 are the
+// three waves' first stages); 4 x 9K, up to 777 new tokens, window 512, 8 over 1 heads,
+// d = 256: 42 us, 310 TFLOP/s, two waves of one CTA per SM.  With 2 splits a unit
+// and one wave (128 CTAs) the first took 127.  REP by the rows a chunk may have:
+// 8 x 20K, 8 tokens (32 rows): 99 us with four copies, 112 with two or one; 8 x 16K,
+// d = 64, 4 tokens (32 rows): 70, 82 and 86, 8 tokens (64 rows): 83 with two, 88 with
+// one; d = 256, 16 x 9K, 8 tokens (64 rows): 38 and 41.  Two copies at d = 128 win
+// where a CTA has few stages and lose where it has many: 8 x 2000, 16 tokens
+// (64 rows): 22.6 us and 23.1; 16 x 4000, 60 tokens, 16 over 16 heads, window 512:
+// 27.8 and 29.4; 40 x 3000, 16 tokens: 107 and 105; 8 x 20K, 9 tokens: 113.1 and 112.2
+// (d = 128 with two copies spills 12 bytes, d = 64 with one or two 8 to 36).
+// Against the two-tile kernel, 8 x 20K: 33 tokens (two tiles) 228 us and 186 there.
 namespace one {
 constexpr int kConvWarp0 = 4;              // warps 4-11 convert
 constexpr int kConv = 8 * 32;
@@ -743,9 +746,12 @@ __global__ void __launch_bounds__(one::kThreads, 1) paged_prefill_one_kernel(con
 //
 // What bounds it: the round trip of a tile -- its warps weigh a stage (about
 // 2600 cycles, of which each of the two reads of S waits for the MMAs in
-// flight), then the tensor cores run its MMAs -- next to which they are 46%
-// busy.  8 x 20K, chunks of 512 tokens (1.35 TFLOP): 1375 us, 983 TFLOP/s.  The
-// MMAs and hand-overs alone take 980 us, all but the softmax 1065.  The same with
+// flight), then the tensor cores run its MMAs -- next to which they are 48%
+// busy.  8 x 20K, chunks of 512 tokens (1.35 TFLOP): 1397 us back to back,
+// 968 TFLOP/s (1375 when the clocks were a little higher, which the figures below
+// compare with); 8 x 16K, 64 over 8 heads, d = 64, 512 tokens each (1.06 TFLOP):
+// 1742 us, 607 TFLOP/s.  The MMAs and hand-overs alone take 980 us of the first,
+// all but the softmax 1065.  The same with
 //   * one hand-over of P a stage, not two: 1433 us;
 //   * stages of 64 keys with two S buffers a tile: 1819 us when this kernel took
 //     1464.  At N = 64 the score MMAs read Q from shared memory twice as often

@@ -29,9 +29,9 @@
 // columns, free of bank conflicts), and serve all heads.
 //
 // Measured: rope_append_kernel, 16,000 tokens of 64 + 2 x 8 heads of 64 into bf16
-// pages (328 MB): 55.4 us, 5.9 TB/s; rope_append_block_kernel, 8 x 2000 tokens of
-// 32 + 2 x 8 heads of 128 (361 MB): 66.7 us, 5.4 TB/s; a decode step of 8 tokens
-// 4.2 and 5.3 us, the launch and a chain of loads.  128-thread CTAs took 67 and
+// pages (328 MB): 54.7 us, 6.0 TB/s; rope_append_block_kernel, 8 x 2000 tokens of
+// 32 + 2 x 8 heads of 128 (361 MB): 66.9 us, 5.4 TB/s; a decode step of 8 tokens
+// 4.1 and 5.4 us, the launch and a chain of loads.  128-thread CTAs took 67 and
 // 70 us, five CTAs per SM (48 registers) 80 in the second, three query items in
 // flight 63 in the first.
 #include <cuda_runtime.h>

@@ -579,7 +579,8 @@ fp8kv_status fp8kv_paged_decode_block(const void* q, const uint8_t* k_cache, con
  * fp8kv_paged_prefill over a block-scaled cache (append the chunk first, with
  * fp8kv_rope_append_block).  Weights are rounded as fp8kv_paged_decode_block's,
  * with less room: relative to themselves down to 2^-14 of a row's largest, in
- * steps of 2^-24 of it below.  All other arguments, the workspace
+ * steps of 2^-24 of it below.  Scores, in units of a factor of two, of up to
+ * 2^26 in size; larger ones may give infinities.  All other arguments, the workspace
  * (fp8kv_paged_prefill_workspace_size) and the errors as fp8kv_paged_prefill.
  * What a row may not attend does not reach it, with one exception, as in
  * fp8kv_paged_prefill: a NaN code in V makes NaN of its dimension in every
