@@ -129,7 +129,7 @@ def attention(q, k, v, vscale, positions, sm, window=0):
     Returns the outputs [R, Hq, d] and what an error bound is made of:
     ``size`` sum p |v| / sum p; ``tiny`` and ``tiny_w``, what 2^-25 of the
     largest probability (of the largest p * vscale, vscale [L, H]) on every key
-    amounts to; ``score`` the largest sm * sum |q k| of a row."""
+    amounts to; ``score`` the largest |sm| * sum |q k| of a row."""
     R, hq, d = q.shape
     g = hq // k.shape[1]
     out, size = np.zeros(q.shape), np.zeros(q.shape)
@@ -148,5 +148,5 @@ def attention(q, k, v, vscale, positions, sm, window=0):
             size[r, h] = p @ np.abs(vv) / l
             tiny[r, h] = 2.0 ** -25 * np.abs(vv).sum(0) / l
             tiny_w[r, h] = 2.0 ** -25 * (p * vs).max() * (np.abs(vv) / vs[:, None]).sum(0) / l
-            score[r, h] = sm * (np.abs(kk) @ np.abs(q[r, h])).max()
+            score[r, h] = abs(sm) * (np.abs(kk) @ np.abs(q[r, h])).max()
     return out, size, tiny, tiny_w, score

@@ -79,3 +79,12 @@ def test_attention_matches_the_scalar_oracle():
     k, v = oracle.e4m3_decode(kc) * np.float32(0.01), oracle.e4m3_decode(vc) * np.float32(0.02)
     out = rb.attention(rb.bf16(q), k, v, np.full((L, hkv), 0.02), [L - 1], 0.25, 20)[0]
     assert np.abs(out - ref).max() < 1e-9
+
+
+def test_a_negative_score_scale_has_the_bound_of_its_size():
+    """Queries and the score scale negated together: the same answer, and the same sizes to bound errors by."""
+    g = np.random.default_rng(4)
+    q, k, v = g.standard_normal((2, 4, 16)), g.standard_normal((20, 2, 16)), g.standard_normal((20, 2, 16))
+    for a, b in zip(rb.attention(q, k, v, np.ones((20, 2)), [15, 19], 0.3),
+                    rb.attention(-q, k, v, np.ones((20, 2)), [15, 19], -0.3)):
+        assert np.array_equal(a, b)
