@@ -102,6 +102,13 @@ def load(build_if_missing: bool = False):
                                               P]
     lib.fp8kv_debug_paged_prefill_block_stall.restype = I
     lib.fp8kv_debug_paged_prefill_block_stall.argtypes = lib.fp8kv_paged_prefill_block.argtypes + [I, U64]
+    tree = [P, I64, P, P, I64, P, I, P, P, P, I, I, I, I, I, I, I, I, F, F, P, P, F, I, P, P, SZ, P]
+    lib.fp8kv_paged_tree_attention.restype = I
+    lib.fp8kv_paged_tree_attention.argtypes = tree
+    lib.fp8kv_debug_paged_tree_stall.restype = I
+    lib.fp8kv_debug_paged_tree_stall.argtypes = tree + [I, U64]
+    lib.fp8kv_paged_tree_workspace_size.restype = SZ
+    lib.fp8kv_paged_tree_workspace_size.argtypes = [I, I, I, I, I, I, I, I]
     _lib = lib
     return lib
 
@@ -747,6 +754,180 @@ def fp8kv_paged_prefill_block(q, k_cache, v_cache, k_scales, v_scales, block_tab
         raise Fp8kvError("fp8kv_paged_prefill_block", code)
 
 
+# ---------------------------------------------------------------- drafted trees, attention weights, eviction
+
+def _cache_ptrs(k_cache, v_cache, cache_format, dev):
+    kind = _BF16 if cache_format == CACHE_BF16 else _U8
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("the caches differ in shape")
+    return _ptr(k_cache, kind, dev, "k_cache"), _ptr(v_cache, kind, dev, "v_cache")
+
+
+def _head_scales(k_scales, v_scales, hkv, dev):
+    if k_scales is None and v_scales is None:
+        return None, None
+    if k_scales is None or v_scales is None or k_scales.numel() != hkv or v_scales.numel() != hkv:
+        raise ValueError("k_scales and v_scales must be [Hkv], both or neither")
+    return _ptr(k_scales, _F32, dev, "k_scales"), _ptr(v_scales, _F32, dev, "v_scales")
+
+
+def _table(block_tables, batch, dev):
+    shape = block_tables.shape
+    if len(shape) != 2 or shape[0] != batch:
+        raise ValueError("block_tables must be [B, max_blocks]")
+    return _ptr(block_tables, _I32, dev, "block_tables"), shape[1]
+
+
+def fp8kv_paged_tree_workspace_size(batch, max_nodes, max_seq_len, num_q_heads, num_kv_heads, head_dim, block_size=16,
+                                    window=0) -> int:
+    n = load().fp8kv_paged_tree_workspace_size(int(batch), int(max_nodes), int(max_seq_len), int(num_q_heads),
+                                               int(num_kv_heads), int(head_dim), int(block_size), int(window))
+    if n == 0:
+        raise Fp8kvError("fp8kv_paged_tree_workspace_size", 1)
+    return int(n)
+
+
+def alloc_tree_workspace(batch, max_nodes, max_seq_len, num_q_heads, num_kv_heads, head_dim, block_size=16, window=0,
+                         device=None, stream=None):
+    """Allocates (through torch) and zero-fills a workspace of fp8kv_paged_tree_attention for these sizes."""
+    n = fp8kv_paged_tree_workspace_size(batch, max_nodes, max_seq_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                                        window)
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    fp8kv_workspace_init(ws, stream)
+    return ws
+
+
+def _tree_args(q, k_cache, v_cache, block_tables, seq_lens, q_starts, parents, max_nodes, max_seq_len, sm_scale, window,
+               out, workspace, k_scale, v_scale, cache_format, k_scales, v_scales, stream):
+    T, hq, d = q.shape
+    nb, hkv, bs, d2 = k_cache.shape
+    B = seq_lens.numel()
+    if d2 != d or out.shape != q.shape:
+        raise ValueError("shape mismatch between q, out and the caches")
+    if q_starts.numel() != B + 1 or parents.numel() != T:
+        raise ValueError("q_starts must be [B + 1] and parents [T]")
+    dev, st = _where(stream, k_cache)
+    return (_ptr(q, _BF16, dev, "q"), T, *_cache_ptrs(k_cache, v_cache, cache_format, dev), nb,
+            *_table(block_tables, B, dev), _ptr(seq_lens, _I32, dev, "seq_lens"), _ptr(q_starts, _I32, dev, "q_starts"),
+            _ptr(parents, _I32, dev, "parents"), int(max_nodes), int(max_seq_len), B, hq, hkv, d, bs, int(cache_format),
+            float(k_scale), float(v_scale), *_head_scales(k_scales, v_scales, hkv, dev), float(sm_scale), int(window),
+            _ptr(out, _BF16, dev, "out"), _ptr(workspace, _U8, dev, "workspace"), workspace.numel(), st)
+
+
+def fp8kv_paged_tree_attention(q, k_cache, v_cache, block_tables, seq_lens, q_starts, parents, max_nodes, max_seq_len,
+                               sm_scale, window, out, workspace, k_scale=1.0, v_scale=1.0, cache_format=CACHE_E4M3,
+                               k_scales=None, v_scales=None, stream=None):
+    """Attention of a tree of drafted tokens per sequence: q, out bf16
+    [sum n, Hq, D], the trees' nodes packed by sequence (q_starts int32 [B + 1]);
+    parents int32 [sum n], each node's parent in its tree or -1.  The nodes are
+    the newest tokens of seq_lens int32 [B].  Caches uint8
+    [num_blocks, Hkv, 16, D] (bf16 for CACHE_BF16)."""
+    code = load().fp8kv_paged_tree_attention(*_tree_args(
+        q, k_cache, v_cache, block_tables, seq_lens, q_starts, parents, max_nodes, max_seq_len, sm_scale, window, out,
+        workspace, k_scale, v_scale, cache_format, k_scales, v_scales, stream))
+    if code:
+        raise Fp8kvError("fp8kv_paged_tree_attention", code)
+
+
+def _lens_out(new_lens, batch, dev):
+    if new_lens.numel() != batch:
+        raise ValueError("new_lens must be [B]")
+    return _ptr(new_lens, _I32, dev, "new_lens")
+
+
+def _format_of(k_cache):
+    """Rows that only move: the width of an element is what matters."""
+    return CACHE_BF16 if k_cache.dtype is _BF16 else CACHE_E4M3
+
+
+def fp8kv_tree_commit(k_cache, v_cache, block_tables, seq_lens, q_starts, accepted, max_seq_len, new_lens, workspace,
+                      stream=None):
+    """Moves the accepted nodes' rows behind each sequence's context: accepted
+    int32 [B, max_accepted], rising node numbers, -1 behind the last; new_lens
+    int32 [B] is written.  Other shapes as fp8kv_paged_tree_attention."""
+    nb, hkv, bs, d = k_cache.shape
+    B = seq_lens.numel()
+    if q_starts.numel() != B + 1 or accepted.dim() != 2 or accepted.shape[0] != B:
+        raise ValueError("q_starts must be [B + 1] and accepted [B, max_accepted]")
+    dev, st = _where(stream, k_cache)
+    kind = _format_of(k_cache)
+    code = load().fp8kv_tree_commit(
+        *_cache_ptrs(k_cache, v_cache, kind, dev), nb, *_table(block_tables, B, dev),
+        _ptr(seq_lens, _I32, dev, "seq_lens"), _ptr(q_starts, _I32, dev, "q_starts"),
+        _ptr(accepted, _I32, dev, "accepted"), accepted.shape[1], int(max_seq_len), B, hkv, d, bs, kind,
+        _lens_out(new_lens, B, dev), _ptr(workspace, _U8, dev, "workspace"), workspace.numel(), st)
+    if code:
+        raise Fp8kvError("fp8kv_tree_commit", code)
+
+
+def fp8kv_paged_decode_weights_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, max_seq_len, block_size=16,
+                                              window=0) -> int:
+    n = load().fp8kv_paged_decode_weights_workspace_size(int(batch), int(num_q_heads), int(num_kv_heads), int(head_dim),
+                                                         int(max_seq_len), int(block_size), int(window))
+    if n == 0:
+        raise Fp8kvError("fp8kv_paged_decode_weights_workspace_size", 1)
+    return int(n)
+
+
+def alloc_weights_workspace(batch, num_q_heads, num_kv_heads, head_dim, max_seq_len, block_size=16, window=0,
+                            device=None, stream=None):
+    """Allocates (through torch) and zero-fills a workspace of fp8kv_paged_decode_weights for these sizes."""
+    n = fp8kv_paged_decode_weights_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, max_seq_len, block_size,
+                                                  window)
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    fp8kv_workspace_init(ws, stream)
+    return ws
+
+
+def _weights_ptr(weights, cache_shape, dev):
+    if weights.shape != cache_shape[:3]:
+        raise ValueError("weights must be [num_blocks, Hkv, block_size]")
+    return _ptr(weights, _F32, dev, "weights")
+
+
+def fp8kv_paged_decode_weights(q, k_cache, v_cache, block_tables, seq_lens, max_seq_len, sm_scale, window, out, weights,
+                               decay, workspace, k_scale=1.0, v_scale=1.0, cache_format=CACHE_E4M3, k_scales=None,
+                               v_scales=None, stream=None):
+    """Decode attention that adds up each cached token's attention weight:
+    weights fp32 [num_blocks, Hkv, 16] becomes weights * decay + the kv head's
+    probabilities (the newest token starts at 0).  Other shapes as
+    fp8kv_paged_decode; caches of any format."""
+    B, hq, d = q.shape
+    nb, hkv, bs, d2 = k_cache.shape
+    if d2 != d or out.shape != q.shape or seq_lens.numel() != B:
+        raise ValueError("shape mismatch between q, out, seq_lens and the caches")
+    dev, st = _where(stream, k_cache)
+    code = load().fp8kv_paged_decode_weights(
+        _ptr(q, _BF16, dev, "q"), *_cache_ptrs(k_cache, v_cache, cache_format, dev), nb, *_table(block_tables, B, dev),
+        _ptr(seq_lens, _I32, dev, "seq_lens"), int(max_seq_len), B, hq, hkv, d, bs, int(cache_format), float(k_scale),
+        float(v_scale), *_head_scales(k_scales, v_scales, hkv, dev), float(sm_scale), int(window),
+        _ptr(out, _BF16, dev, "out"), _weights_ptr(weights, k_cache.shape, dev), float(decay),
+        _ptr(workspace, _U8, dev, "workspace"), workspace.numel(), st)
+    if code:
+        raise Fp8kvError("fp8kv_paged_decode_weights", code)
+
+
+def fp8kv_evict(k_cache, v_cache, weights, block_tables, seq_lens, max_seq_len, budget, sinks, recent, new_lens,
+                workspace, kept=None, stream=None):
+    """Cuts every sequence back to `budget` tokens per kv head: the first
+    `sinks`, the last `recent` and those of the largest weights move to the front
+    of its pages, in their order; new_lens int32 [B] is written, and kept int32
+    [B, Hkv, budget] where given (the places they had, -1 past new_lens)."""
+    nb, hkv, bs, d = k_cache.shape
+    B = seq_lens.numel()
+    if kept is not None and tuple(kept.shape) != (B, hkv, budget):
+        raise ValueError("kept must be [B, Hkv, budget]")
+    dev, st = _where(stream, k_cache)
+    kind = _format_of(k_cache)
+    code = load().fp8kv_evict(
+        *_cache_ptrs(k_cache, v_cache, kind, dev), _weights_ptr(weights, k_cache.shape, dev), nb,
+        *_table(block_tables, B, dev), _ptr(seq_lens, _I32, dev, "seq_lens"), int(max_seq_len), int(budget), int(sinks),
+        int(recent), B, hkv, d, bs, kind, _lens_out(new_lens, B, dev), _opt(kept, _I32, dev, "kept"),
+        _ptr(workspace, _U8, dev, "workspace"), workspace.numel(), st)
+    if code:
+        raise Fp8kvError("fp8kv_evict", code)
+
+
 # ---------------------------------------------------------------- failure-path test hooks
 
 def debug_paged_decode_stall(q, k_cache, v_cache, block_tables, seq_lens, max_seq_len, k_scale, v_scale, sm_scale,
@@ -778,3 +959,13 @@ def debug_paged_prefill_block_stall(q, k_cache, v_cache, k_scales, v_scales, blo
     return load().fp8kv_debug_paged_prefill_block_stall(*_prefill_block_args(
         q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, q_starts, max_q_len, max_seq_len, sm_scale,
         window, out, workspace, stream), int(stall_stage), int(wait_limit_ns))
+
+
+def debug_paged_tree_stall(q, k_cache, v_cache, block_tables, seq_lens, q_starts, parents, max_nodes, max_seq_len,
+                           sm_scale, window, out, workspace, stall_stage, wait_limit_ns, k_scale=1.0, v_scale=1.0,
+                           cache_format=CACHE_E4M3, k_scales=None, v_scales=None, stream=None) -> int:
+    """fp8kv_debug_paged_tree_stall: the tree attention with the score MMAs of
+    stage `stall_stage` of CTA 0 never issued.  Returns the launch status."""
+    return load().fp8kv_debug_paged_tree_stall(*_tree_args(
+        q, k_cache, v_cache, block_tables, seq_lens, q_starts, parents, max_nodes, max_seq_len, sm_scale, window, out,
+        workspace, k_scale, v_scale, cache_format, k_scales, v_scales, stream), int(stall_stage), int(wait_limit_ns))

@@ -48,6 +48,54 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n) {
     return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+// Shared-memory matrix descriptor of a K-major operand whose rows are 64 bytes,
+// swizzled within 64 (chunk index XOR row pair; 8-row groups 512 bytes apart,
+// layout type 4).
+__device__ __forceinline__ uint64_t desc_k_sw64(uint32_t saddr) {
+    uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(1) << 16;
+    d |= static_cast<uint64_t>(512 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(4) << 61;
+    return d;
+}
+
+// The descriptor of an operand whose rows run along K (MN-major), 128-byte
+// swizzle: row k holds 64 16-bit elements of the M or N dimension, its chunk c
+// at k * 128 + ((c ^ (k & 7)) * 16); 8-row groups follow each other (1024
+// bytes, the stride offset), blocks of 64 elements lie `block` bytes apart
+// (the leading-dimension offset).  A step of K = 16 rows is 2048 bytes.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t block) {
+    uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((block >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+// Instruction descriptors with an FP32 accumulator (fields as idesc_f16_f32):
+// kind::f16 with both operands f16 or both bf16 (format 1), B K-major or, with
+// `b_mn`, MN-major (bit 16); kind::f8f6f4 with A of E4M3 (format 0) and B of
+// E4M3 or E5M2 (format 1), both K-major.
+__host__ __device__ constexpr uint32_t idesc_16bit(int m, int n, bool bf16, bool b_mn) {
+    return idesc_f16_f32(m, n) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u);
+}
+__host__ __device__ constexpr uint32_t idesc_fp8(int m, int n, bool b_e5m2) {
+    return idesc_f16_f32(m, n) | (b_e5m2 ? 1u << 10 : 0u);
+}
+
+// mma_f16 for 8-bit operands, K = 32 (32 bytes of a row).
+__device__ __forceinline__ void mma_fp8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // D[tmem] (+)= A * B^T for an M x K tile of A and an N x K tile of B (both
 // K-major in shared memory), K = 16; `accumulate` == 0 overwrites D.
 // Issued by one thread.

@@ -596,6 +596,71 @@ fp8kv_status fp8kv_paged_prefill_block(const void* q, int64_t num_q_tokens, cons
                                        size_t workspace_bytes, void* stream);
 
 /*
+ * Attention of a tree of drafted tokens per sequence (speculative decoding:
+ * a draft proposes several continuations at once, one call checks them all).
+ * No counterpart on the pages; it stands beside fp8kv_paged_prefill, whose
+ * chunk is the tree that is one chain.
+ *
+ * Sequence b holds L = seq_lens[b] tokens in the cache, the newest
+ * n = q_starts[b+1] - q_starts[b] of them its drafted nodes, in any order that
+ * has parents before children (append them first, at slots L - n + i, rotated
+ * by the position c + depth(i) they stand for, c = L - n).  parents[q_starts[b]
+ * + i] is the node's parent, a smaller number of the same tree, or -1: a root,
+ * of depth 0; a child's depth is its parent's plus 1.  Node i attends
+ *   - the context: token t < c with t > c + depth(i) - window;
+ *   - itself and its ancestors j with depth(j) > depth(i) - window
+ * (window <= 0: all of them), with the scores, softmax and rounding of
+ * fp8kv_paged_prefill.  The newest keys before them in the cache are other
+ * branches; they do not reach the row, but for a NaN or infinity in V, which
+ * makes NaN of its dimension in every row that shares a tile (up to 256 rows:
+ * node, query head), since a weight of zero still multiplies it.
+ *
+ *   q, out         bf16 [num_tokens][num_q_heads][head_dim], 16-byte aligned,
+ *                  packed by sequence.  Rows that belong to no sequence are
+ *                  left as they are.
+ *   k_cache,       [num_blocks][num_kv_heads][block_size][head_dim] of
+ *   v_cache        cache_format (fp8kv_cache_format), 16-byte aligned
+ *   block_tables   as fp8kv_paged_decode
+ *   seq_lens       int32 [batch] on the device
+ *   q_starts       int32 [batch + 1] on the device, non-decreasing
+ *   parents        int32 [num_tokens] on the device
+ *   max_nodes      host-side bound of the trees' sizes, at most 256
+ *   k_scale ..     as fp8kv_rope_append: per-tensor scales (1 for a bf16 cache),
+ *   v_scales       or DEVICE fp32 [num_kv_heads] arrays in their place (null
+ *                  for a bf16 cache)
+ *   window         as above
+ *   workspace      >= fp8kv_paged_tree_workspace_size(...) bytes, 256-byte
+ *                  aligned, zero-filled before first use (fp8kv_workspace_init).
+ *                  Calls that share it must be ordered.  Its error word
+ *                  (fp8kv_read_error) says FP8KV_ERR_INVALID_ARG for a block id
+ *                  out of range (block 0 is read), for a parent that is neither
+ *                  -1 nor a smaller node (it counts as -1), and for lengths or
+ *                  starts out of bounds (0 <= n <= min(seq_lens[b], max_nodes),
+ *                  seq_lens[b] <= max_seq_len, rows within num_tokens: the
+ *                  sequence is clamped, or skipped if its rows do not exist).
+ *                  FP8KV_ERR_TIMEOUT as for the other calls.
+ * Queries enter an FP8 cache's score MMAs as two E4M3 numbers, which hold a
+ * bf16 exactly down to 2^-15 of the row's largest element and to 2^-17 of that
+ * below.  Weights are f16 (11 bits down to 2^-23 of the row's largest, steps of
+ * 2^-33 of it below); over a bf16 cache two bf16 numbers.
+ * Supported: head_dim in {64, 128, 256}; block_size == 16; g in {1, 2, 4, 8, 16};
+ *            max_nodes <= 256; num_blocks * num_kv_heads < 2^31.  batch == 0,
+ *            max_nodes == 0 or num_tokens == 0 is a no-op.
+ */
+fp8kv_status fp8kv_paged_tree_attention(const void* q, int64_t num_tokens, const void* k_cache, const void* v_cache,
+                                        int64_t num_blocks, const int32_t* block_tables, int max_blocks_per_seq,
+                                        const int32_t* seq_lens, const int32_t* q_starts, const int32_t* parents,
+                                        int max_nodes, int max_seq_len, int batch, int num_q_heads, int num_kv_heads,
+                                        int head_dim, int block_size, int cache_format, float k_scale, float v_scale,
+                                        const float* k_scales, const float* v_scales, float sm_scale, int window,
+                                        void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of fp8kv_paged_tree_attention on the CURRENT device; 0 if the
+ * arguments are invalid or no device is available. */
+size_t fp8kv_paged_tree_workspace_size(int batch, int max_nodes, int max_seq_len, int num_q_heads, int num_kv_heads,
+                                       int head_dim, int block_size, int window);
+
+/*
  * Failure-path test hooks.  No counterpart on the pages: the pages' failure
  * mode is silent (a wrong answer, no error), and these make the library's
  * answer to a stall observable.  A kernel wait that runs out writes
@@ -642,6 +707,18 @@ fp8kv_status fp8kv_debug_paged_prefill_block_stall(
     const int32_t* seq_lens, const int32_t* q_starts, int max_q_len, int max_seq_len, int batch, int num_q_heads,
     int num_kv_heads, int head_dim, int block_size, float sm_scale, int window, void* out, void* workspace,
     size_t workspace_bytes, void* stream, int stall_stage, uint64_t wait_limit_ns);
+
+/* The same hook for fp8kv_paged_tree_attention: CTA 0 never issues the score
+ * MMAs of its stage `stall_stage`. */
+fp8kv_status fp8kv_debug_paged_tree_stall(const void* q, int64_t num_tokens, const void* k_cache, const void* v_cache,
+                                          int64_t num_blocks, const int32_t* block_tables, int max_blocks_per_seq,
+                                          const int32_t* seq_lens, const int32_t* q_starts, const int32_t* parents,
+                                          int max_nodes, int max_seq_len, int batch, int num_q_heads,
+                                          int num_kv_heads, int head_dim, int block_size, int cache_format,
+                                          float k_scale, float v_scale, const float* k_scales, const float* v_scales,
+                                          float sm_scale, int window, void* out, void* workspace,
+                                          size_t workspace_bytes, void* stream, int stall_stage,
+                                          uint64_t wait_limit_ns);
 
 #ifdef __cplusplus
 }
