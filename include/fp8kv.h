@@ -661,6 +661,69 @@ size_t fp8kv_paged_tree_workspace_size(int batch, int max_nodes, int max_seq_len
                                        int head_dim, int block_size, int window);
 
 /*
+ * After a tree is checked: the accepted path's rows of K and V move behind the
+ * context, in every kv head.  The path's i-th node lies at token c + accepted[i]
+ * and moves to c + i (c = L - n as above); keys keep the rotation they were
+ * stored with, which is that of their new place.  Rows from c + count on are
+ * left as they are.
+ *
+ *   accepted       int32 [batch][max_accepted] on the device: node numbers in
+ *                  strictly rising order, ended by the first negative entry
+ *                  (or by max_accepted).  count is their number, 0 allowed.
+ *   new_lens       int32 [batch] on the device, written: c + count.  Not
+ *                  seq_lens itself, which the next layer's call still needs.
+ *   k_cache ..     as fp8kv_paged_tree_attention (whose scales do not matter:
+ *   max_seq_len    rows move as they are)
+ *   workspace      256-byte aligned, at least 256 bytes, zero-filled before first
+ *                  use: the error word.  FP8KV_ERR_INVALID_ARG: a block id out of
+ *                  range (rows from it or to it are not moved), lengths or starts
+ *                  out of bounds (clamped as above, n to at most 256), an entry
+ *                  of accepted that does not rise or is not below n (it ends
+ *                  the path).
+ * Supported: head_dim in {64, 128, 256}; block_size == 16; batch <= 65535;
+ *            num_kv_heads <= 65535; max_accepted <= 256; num_blocks * num_kv_heads
+ *            < 2^31.  A page that two sequences share must hold no row that
+ *            either moves.  batch == 0 or max_accepted == 0 is a no-op (new_lens is
+ *            not written).
+ */
+fp8kv_status fp8kv_tree_commit(void* k_cache, void* v_cache, int64_t num_blocks, const int32_t* block_tables,
+                               int max_blocks_per_seq, const int32_t* seq_lens, const int32_t* q_starts,
+                               const int32_t* accepted, int max_accepted, int max_seq_len, int batch, int num_kv_heads,
+                               int head_dim, int block_size, int cache_format, int32_t* new_lens, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * Cuts every sequence back to `budget` tokens by accumulated attention weight,
+ * each kv head for itself (a page holds one head's rows, so heads may keep
+ * different tokens).  Of sequence b's L = seq_lens[b] tokens, where L > budget, kv
+ * head hk keeps the first `sinks`, the last `recent`, and of the others the
+ * budget - sinks - recent of the largest weights[page(t)][hk][t % bs]; of equal
+ * weights the earlier token (-0 equals 0, a NaN is below every number).  The kept
+ * rows of K, V and weights move to places 0 .. budget - 1 of the sequence, in
+ * their order; rows from there on are left as they are.  Where L <= budget
+ * nothing moves.  Keys keep the rotation of their old position: later tokens are
+ * rotated by their true positions, not by their place.
+ *
+ *   weights        fp32 [num_blocks][num_kv_heads][block_size], 16-byte aligned
+ *   budget         >= 1; sinks >= 0, recent >= 0, sinks + recent <= budget
+ *   new_lens       int32 [batch] on the device, written: min(L, budget).  Not
+ *                  seq_lens itself.
+ *   kept           int32 [batch][num_kv_heads][budget] on the device, or null:
+ *                  written with the places the kept tokens had, -1 past new_lens
+ *   workspace      as fp8kv_tree_commit.  FP8KV_ERR_INVALID_ARG: a block id out of
+ *                  range (its weights count as 0 and its rows are not moved,
+ *                  nor any into its place), a length outside [0, max_seq_len]
+ *                  (clamped).
+ *   all other arguments as fp8kv_tree_commit
+ * Supported: as fp8kv_tree_commit; max_seq_len <= 393,216.  A page must be in one
+ * place of one sequence's row only.  batch == 0 is a no-op.
+ */
+fp8kv_status fp8kv_evict(void* k_cache, void* v_cache, float* weights, int64_t num_blocks, const int32_t* block_tables,
+                         int max_blocks_per_seq, const int32_t* seq_lens, int max_seq_len, int budget, int sinks,
+                         int recent, int batch, int num_kv_heads, int head_dim, int block_size, int cache_format,
+                         int32_t* new_lens, int32_t* kept, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Failure-path test hooks.  No counterpart on the pages: the pages' failure
  * mode is silent (a wrong answer, no error), and these make the library's
  * answer to a stall observable.  A kernel wait that runs out writes

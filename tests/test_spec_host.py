@@ -1,4 +1,4 @@
-"""Drafted trees without a GPU: the C ABI refuses bad arguments before it touches the device, the binding refuses
+"""Drafted trees and eviction without a GPU: the C ABI refuses bad arguments before it touches the device, the binding refuses
 shapes that do not fit and tensors that are not on one, and the cut of a tree's work over CTAs is whole."""
 import ctypes
 import os
@@ -142,3 +142,58 @@ def test_every_page_of_every_unit_is_walked_once(tmp_path):
     csrc = os.path.join(os.path.dirname(fbuild.__file__), "csrc")
     subprocess.run(["g++", "-O1", "-std=c++17", "-I", csrc, str(src), "-o", str(exe)], check=True)
     assert subprocess.run([str(exe)]).returncode == 0
+
+
+def _commit(lib, **kw):
+    a = dict(k=FAKE, v=FAKE, nb=100, bt=FAKE, mb=8, sl=FAKE, st=FAKE, acc=FAKE, n=16, msl=128, B=2, hkv=8, d=128, bs=16,
+             fmt=0, new=FAKE, ws=FAKE, wsb=256)
+    a.update(kw)
+    return lib.fp8kv_tree_commit(a["k"], a["v"], a["nb"], a["bt"], a["mb"], a["sl"], a["st"], a["acc"], a["n"], a["msl"],
+                                 a["B"], a["hkv"], a["d"], a["bs"], a["fmt"], a["new"], a["ws"], a["wsb"], None)
+
+
+def _evict(lib, **kw):
+    a = dict(k=FAKE, v=FAKE, w=FAKE, nb=100, bt=FAKE, mb=8, sl=FAKE, msl=128, budget=64, sinks=4, recent=16, B=2, hkv=8,
+             d=128, bs=16, fmt=0, new=FAKE, kept=None, ws=FAKE, wsb=256)
+    a.update(kw)
+    return lib.fp8kv_evict(a["k"], a["v"], a["w"], a["nb"], a["bt"], a["mb"], a["sl"], a["msl"], a["budget"], a["sinks"],
+                           a["recent"], a["B"], a["hkv"], a["d"], a["bs"], a["fmt"], a["new"], a["kept"], a["ws"], a["wsb"],
+                           None)
+
+
+MOVES = [(dict(new=None), 1), (dict(new=OFF2), 1), (dict(ws=None), 3), (dict(ws=OFF4), 3), (dict(wsb=255), 3)]
+
+
+@pytest.mark.parametrize("kw,code", SHAPES + MOVES + [
+    (dict(st=None), 1), (dict(st=OFF2), 1), (dict(acc=None), 1), (dict(acc=OFF2), 1), (dict(n=-1), 1), (dict(n=257), 2),
+    (dict(B=0, k=None, ws=None), 0), (dict(n=0, k=None, ws=None), 0), (dict(n=0, B=-1), 1),
+])
+def test_tree_commit_validates(lib, kw, code):
+    assert _commit(lib, **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", SHAPES + MOVES + [
+    (dict(w=None), 1), (dict(w=OFF4), 1), (dict(kept=OFF2), 1), (dict(budget=0), 1), (dict(sinks=-1), 1),
+    (dict(recent=-1), 1), (dict(sinks=40, recent=25), 1), (dict(sinks=2**31 - 1, recent=2**31 - 1), 1),
+    (dict(msl=393217, mb=30000), 2), (dict(B=0, k=None, w=None, ws=None), 0),
+])
+def test_evict_validates(lib, kw, code):
+    assert _evict(lib, **kw) == code
+
+
+def test_binding_refuses_what_commit_and_evict_cannot_take():
+    cache, ws = torch.zeros((3, 2, 16, 64), dtype=torch.uint8), torch.zeros(256, dtype=torch.uint8)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    ok = dict(k_cache=cache, v_cache=cache, block_tables=i32(2, 3), seq_lens=i32(2), q_starts=i32(3), accepted=i32(2, 4),
+              max_seq_len=40, new_lens=i32(2), workspace=ws)
+    with pytest.raises(TypeError):
+        fk.fp8kv_tree_commit(**ok)
+    for bad in (dict(q_starts=i32(2)), dict(accepted=i32(3, 4)), dict(accepted=i32(2))):
+        with pytest.raises(ValueError):
+            fk.fp8kv_tree_commit(**{**ok, **bad})
+    ok = dict(k_cache=cache, v_cache=cache, weights=torch.zeros((3, 2, 16)), block_tables=i32(2, 3), seq_lens=i32(2),
+              max_seq_len=40, budget=8, sinks=1, recent=1, new_lens=i32(2), workspace=ws)
+    with pytest.raises(TypeError):
+        fk.fp8kv_evict(**ok)
+    with pytest.raises(ValueError):
+        fk.fp8kv_evict(**{**ok, "kept": i32(2, 2, 9)})
