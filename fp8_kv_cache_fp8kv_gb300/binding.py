@@ -111,6 +111,11 @@ def load(build_if_missing: bool = False):
     lib.fp8kv_paged_tree_workspace_size.argtypes = [I, I, I, I, I, I, I, I]
     lib.fp8kv_tree_commit.restype = I
     lib.fp8kv_tree_commit.argtypes = [P, P, I64, P, I, P, P, P, I, I, I, I, I, I, I, P, P, SZ, P]
+    lib.fp8kv_paged_decode_weights.restype = I
+    lib.fp8kv_paged_decode_weights.argtypes = [P, P, P, I64, P, I, P, I, I, I, I, I, I, I, F, F, P, P, F, I, P, P, F, P,
+                                               SZ, P]
+    lib.fp8kv_paged_decode_weights_workspace_size.restype = SZ
+    lib.fp8kv_paged_decode_weights_workspace_size.argtypes = [I, I, I, I, I, I, I]
     lib.fp8kv_evict.restype = I
     lib.fp8kv_evict.argtypes = [P, P, P, I64, P, I, P, I, I, I, I, I, I, I, I, I, P, P, P, SZ, P]
     _lib = lib

@@ -1004,6 +1004,36 @@ struct StallHook {
     uint64_t wait_ns;
 };
 
+// What fp8kv_paged_decode_weights adds to a decode.
+struct WeightsOut {
+    float* weights;
+    float decay;
+};
+
+// Sequences per launch of such a decode, and what it needs behind the decode's
+// workspace.  A launch's scores stay within kScoreBytes (they are read back once,
+// so they should not leave the L2), or are one sequence's.
+constexpr int64_t kScoreBytes = INT64_C(64) << 20;
+
+struct ScorePlan {
+    int batch;        // sequences per launch
+    int tokens;       // places a unit's scores take
+    size_t softmax, scores, total;   // bytes from the end of the decode's workspace
+};
+
+ScorePlan score_plan(int batch, int num_q_heads, int max_seq_len, int window) {
+    ScorePlan p;
+    int64_t pages = (static_cast<int64_t>(max_seq_len) + kBS - 1) / kBS;
+    if (window > 0) pages = std::min<int64_t>(pages, (static_cast<int64_t>(window) + kBS - 1) / kBS + 1);
+    p.tokens = static_cast<int>(pages * kBS);
+    const int64_t each = std::max<int64_t>(1, pages * kBS * num_q_heads * static_cast<int64_t>(sizeof(float)));
+    p.batch = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(batch, kMaxBatch), kScoreBytes / each)));
+    p.softmax = 0;
+    p.scores = align256(static_cast<size_t>(p.batch) * num_q_heads * sizeof(float2));
+    p.total = p.scores + align256(static_cast<size_t>(p.batch) * static_cast<size_t>(each));
+    return p;
+}
+
 fp8kv_status decode_impl(const void* q, const void* k_new, const void* v_new, const uint8_t* k_cache,
                          const uint8_t* v_cache, int64_t num_blocks, const int32_t* block_tables,
                          int max_blocks_per_seq, const int32_t* seq_lens, int max_seq_len, int batch,
@@ -1012,7 +1042,8 @@ fp8kv_status decode_impl(const void* q, const void* k_new, const void* v_new, co
                          size_t workspace_bytes, void* stream, int engine, int es = 1,
                          const float* k_scales = nullptr, const float* v_scales = nullptr, bool e5m2 = false,
                          const HostStage* hs = nullptr, const StallHook* dbg = nullptr,
-                         const float* k_page_scales = nullptr, const float* v_page_scales = nullptr) {
+                         const float* k_page_scales = nullptr, const float* v_page_scales = nullptr,
+                         const WeightsOut* wout = nullptr) {
     auto a16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
     if (batch < 0 || batch > 65535 || num_kv_heads < 1 || num_kv_heads > 65535 || num_q_heads < 1 ||
         num_q_heads % num_kv_heads != 0 || max_seq_len < 0 || num_blocks < 1 || max_blocks_per_seq < 0)
@@ -1046,9 +1077,10 @@ fp8kv_status decode_impl(const void* q, const void* k_new, const void* v_new, co
         return FP8KV_ERR_INVALID_ARG;
     int sms = 0;
     if (device_sms(&sms) != 0) return FP8KV_ERR_CUDA;
+    const ScorePlan sp = wout ? score_plan(batch, num_q_heads, max_seq_len, window) : ScorePlan{kMaxBatch, 0, 0, 0, 0};
     const WsLayout w = ws_layout(batch, num_q_heads, hm.units_per_seq, head_dim,
-                                 make_plan(batch, hm.units_per_seq, head_dim, max_seq_len, window, sms));
-    if (!workspace || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+                                 make_plan(std::min(batch, sp.batch), hm.units_per_seq, head_dim, max_seq_len, window, sms));
+    if (!workspace || workspace_bytes < w.total + sp.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return FP8KV_ERR_WORKSPACE;
 
     CUtensorMap mk, mv;  // the CUDA-core engine's TMA view of the caches (rows of head_dim bytes)
@@ -1076,10 +1108,10 @@ fp8kv_status decode_impl(const void* q, const void* k_new, const void* v_new, co
             (void)cudaGetLastError();  // not a registered host buffer: copy instead
         }
     }
-    // Batches above kMaxBatch sequences run as consecutive launches on the
-    // stream, reusing the workspace.
-    for (int b0 = 0; b0 < batch; b0 += kMaxBatch) {
-        const int nb = std::min(kMaxBatch, batch - b0);
+    // Batches above kMaxBatch sequences (or whose scores take more room) run as
+    // consecutive launches on the stream, reusing the workspace.
+    for (int b0 = 0; b0 < batch; b0 += sp.batch) {
+        const int nb = std::min(sp.batch, batch - b0);
         const Plan p = make_plan(nb, hm.units_per_seq, head_dim, max_seq_len, window, sms);
         DecodeArgs a;
         a.q = static_cast<const uint16_t*>(q) + static_cast<int64_t>(b0) * num_q_heads * head_dim;
@@ -1117,8 +1149,15 @@ fp8kv_status decode_impl(const void* q, const void* k_new, const void* v_new, co
         a.v_scale = v_scale;
         a.wait_ns = dbg ? dbg->wait_ns : kWaitLimitNs;
         a.stall_stage = dbg ? dbg->stall_stage : -1;
+        a.scores = wout ? reinterpret_cast<float*>(ws + w.total + sp.scores) : nullptr;
+        a.softmax = wout ? reinterpret_cast<float2*>(ws + w.total + sp.softmax) : nullptr;
+        a.score_tokens = sp.tokens;
+        a.weights = wout ? wout->weights : nullptr;
+        a.decay = wout ? wout->decay : 0.f;
         cudaError_t e;
-        if (!simt) {
+        if (wout) {
+            e = launch_stream_weights(head_dim, G, es, e5m2, a, p.ctas, s);
+        } else if (!simt) {
             if (k_page_scales)
                 e = launch_stream_block(head_dim, G, a, p.ctas, s);
             else if (es == 2)
@@ -1217,6 +1256,39 @@ extern "C" fp8kv_status fp8kv_paged_decode_block(const void* q, const uint8_t* k
                        max_seq_len, batch, num_q_heads, num_kv_heads, head_dim, block_size, 1.0f, 1.0f, sm_scale,
                        window, out, workspace, workspace_bytes, stream, FP8KV_ENGINE_TENSOR_CORES, 1, nullptr, nullptr,
                        false, nullptr, nullptr, k_scales, v_scales);
+}
+
+extern "C" size_t fp8kv_paged_decode_weights_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                                                            int max_seq_len, int block_size, int window) {
+    if (batch < 0 || num_kv_heads < 1 || num_q_heads < 1 || num_q_heads % num_kv_heads != 0 || max_seq_len < 0)
+        return 0;
+    if (!supported(head_dim, block_size, num_q_heads / num_kv_heads)) return 0;
+    int sms = 0;
+    if (device_sms(&sms) != 0) return 0;
+    const HeadMap hm = head_map(num_q_heads, num_kv_heads, head_dim, false);
+    const ScorePlan sp = score_plan(batch, num_q_heads, max_seq_len, window > 0 ? window : 0);
+    const Plan p = make_plan(std::min(batch, sp.batch), hm.units_per_seq, head_dim, max_seq_len, window, sms);
+    return ws_layout(batch, num_q_heads, hm.units_per_seq, head_dim, p).total + sp.total;
+}
+
+extern "C" fp8kv_status fp8kv_paged_decode_weights(
+    const void* q, const void* k_cache, const void* v_cache, int64_t num_blocks, const int32_t* block_tables,
+    int max_blocks_per_seq, const int32_t* seq_lens, int max_seq_len, int batch, int num_q_heads, int num_kv_heads,
+    int head_dim, int block_size, int cache_format, float k_scale, float v_scale, const float* k_scales,
+    const float* v_scales, float sm_scale, int window, void* out, float* weights, float decay, void* workspace,
+    size_t workspace_bytes, void* stream) {
+    FP8KV_TRACE("fp8kv_paged_decode_weights");
+    const bool bf16 = cache_format == FP8KV_CACHE_BF16;
+    if (cache_format != FP8KV_CACHE_E4M3 && cache_format != FP8KV_CACHE_E5M2 && !bf16) return FP8KV_ERR_INVALID_ARG;
+    if (!std::isfinite(decay) || decay < 0.f) return FP8KV_ERR_INVALID_ARG;
+    if (bf16 && (k_scales || v_scales || k_scale != 1.f || v_scale != 1.f)) return FP8KV_ERR_INVALID_ARG;
+    if (batch > 0 && (!weights || (reinterpret_cast<uintptr_t>(weights) & 15u))) return FP8KV_ERR_INVALID_ARG;
+    const WeightsOut wo{weights, decay};
+    return decode_impl(q, nullptr, nullptr, static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache),
+                       num_blocks, block_tables, max_blocks_per_seq, seq_lens, max_seq_len, batch, num_q_heads,
+                       num_kv_heads, head_dim, block_size, k_scale, v_scale, sm_scale, window > 0 ? window : 0, out,
+                       workspace, workspace_bytes, stream, FP8KV_ENGINE_TENSOR_CORES, bf16 ? 2 : 1, k_scales, v_scales,
+                       cache_format == FP8KV_CACHE_E5M2, nullptr, nullptr, nullptr, nullptr, &wo);
 }
 
 extern "C" fp8kv_status fp8kv_decode_step_per_head(const void* q, const void* k_new, const void* v_new,

@@ -72,6 +72,14 @@ struct DecodeArgs {
     // the ring waits give up after wait_ns (normally kWaitLimitNs).
     uint64_t wait_ns;
     int stall_stage;
+    // fp8kv_paged_decode_weights (read by the WS kernels only): the scores in log2
+    // units, token by token from the unit's first attended page on, and each
+    // query head's softmax reference and 1 / sum.
+    float* scores;              // [B*Hkv][score_tokens][G]
+    float2* softmax;            // [B][Hq]
+    int score_tokens;
+    float* weights;             // [num_blocks][cache kv heads][16], updated
+    float decay;
 };
 
 // Geometry of one head dimension D with ES-byte elements (1: E4M3 codes,
@@ -421,12 +429,14 @@ __device__ __forceinline__ void absorb(const float* x, int lane, float (&m)[2], 
 // 32.4, 65.7 and 19.9 (g = 16 at d = 128 now has 255 registers and spills 16 bytes).
 constexpr float kRoom = 15.f;
 
-template <int D, int ES, bool E5M2, int NT, bool BS>
+// WS: the scores go to `score` too, that of token tok_base and the unit's first
+// head first, G of them a token.
+template <int D, int ES, bool E5M2, int NT, bool BS, bool WS = false, int G = 8>
 __device__ __forceinline__ void tc_stage(const uint8_t* kst, const uint8_t* vst, const float2* psc, int np,
                                          int tok_base, int lo, int L,
                                          int gid, int tig, const uint32_t (&qf)[NT][Geo<D, ES>::KS][2],
                                          const float (&cs)[NT][2], float (&m)[NT][2], float (&l)[NT][2],
-                                         float (&o)[NT][Geo<D, ES>::MT][4]) {
+                                         float (&o)[NT][Geo<D, ES>::MT][4], float* score = nullptr) {
     using Gm = Geo<D, ES>;
     constexpr bool kEarlyV = Gm::MT == 8 && NT == 1;
     // ---- (d = 128) the stage's V fragments into registers first, so their
@@ -522,6 +532,12 @@ __device__ __forceinline__ void tc_stage(const uint8_t* kst, const uint8_t* vst,
                     const float x = !valid ? -INFINITY : BS ? fmaf(raw, cs[t][j] * kscale[p], vlog[p]) : raw * cs[t][j];
                     sc[p][t][2 * e2 + j] = x;
                     mx[t][j] = fmaxf(mx[t][j], x);
+                }
+                if constexpr (WS) {
+                    float* to = score + (p * kBS + gid + 8 * e2) * G + 8 * t + 2 * tig;
+                    if (valid && G > 1 && 8 * t + 2 * tig < G)
+                        *reinterpret_cast<float2*>(to) = make_float2(sc[p][t][2 * e2], sc[p][t][2 * e2 + 1]);
+                    if (valid && G == 1 && tig == 0) *to = sc[p][t][2 * e2];
                 }
             }
     }
@@ -636,7 +652,7 @@ __device__ __forceinline__ void tc_stage(const uint8_t* kst, const uint8_t* vst,
 // longer needs) by 16-byte cp.async copies issued all at once; thread i then
 // folds (query head, 4 dims) items i, i + NTHR, ... over the chunk (max, then
 // rescale and accumulate).
-template <int D, int G, int NTHR, int STAGE_BYTES>
+template <int D, int G, int NTHR, int STAGE_BYTES, bool WS = false>
 __device__ __forceinline__ void merge_unit(const DecodeArgs& a, int u, int c_first, int k_u, int tid,
                                            uint8_t* stage) {
     constexpr int NG = D / 4;                      // float4 groups per head
@@ -701,6 +717,8 @@ __device__ __forceinline__ void merge_unit(const DecodeArgs& a, int u, int c_fir
         if (it < ITEMS) {
             const int h = it / NG, g4 = it - (it / NG) * NG;
             const float sc_out = Lh[j] > 0.f ? vsc / Lh[j] : 0.f;
+            if constexpr (WS)
+                if (g4 == 0) a.softmax[static_cast<int64_t>(b) * a.num_q_heads + hk * G + h] = make_float2(M[j], 1.f / Lh[j]);
             uint16_t* out = a.out + (static_cast<int64_t>(b) * a.num_q_heads + hk * G + h) * D;
             const uint32_t lo2 =
                 f32_to_bf16(acc[j].x * sc_out) | (static_cast<uint32_t>(f32_to_bf16(acc[j].y * sc_out)) << 16);
@@ -744,7 +762,7 @@ constexpr size_t stream_smem_bytes() {
 // SM, 1 KB of it reserved per CTA).
 constexpr size_t kSmemPerCta = (228u * 1024u) / kCtasPerSm - 1024u;
 
-template <int D, int G, int ES, bool E5M2, bool BS = false>
+template <int D, int G, int ES, bool E5M2, bool BS = false, bool WS = false>
 __global__ void __launch_bounds__(StreamCfg<D, ES, G>::NW * 32, kCtasPerSm)
     stream_decode_kernel(const DecodeArgs a) {
     using Gm = Geo<D, ES>;
@@ -958,6 +976,11 @@ __global__ void __launch_bounds__(StreamCfg<D, ES, G>::NW * 32, kCtasPerSm)
             cp_async_wait<R - 1>();
             __syncwarp();
             const uint8_t* kst_p = ring + (kst % R) * Gm::SB;
+            if constexpr (WS)
+                tc_stage<D, ES, E5M2, NT, BS, true, G>(
+                    kst_p, kst_p + Gm::SH, scales, min(Gm::PPS, q1 - p0), (pg_first + p0) * kBS, lo, L, gid, tig, qf, cs, m,
+                    l, o, a.scores + (static_cast<int64_t>(w.b * Hkv + w.hk) * a.score_tokens + (lp0 + p0) * kBS) * G);
+            else
             tc_stage<D, ES, E5M2, NT, BS>(kst_p, kst_p + Gm::SH, scales + (kst % R) * Gm::PPS, min(Gm::PPS, q1 - p0),
                                           (pg_first + p0) * kBS, lo, L, gid, tig, qf, cs, m, l, o);
             __syncwarp();  // every lane is done with the slot before it is refilled
@@ -1000,6 +1023,9 @@ __global__ void __launch_bounds__(StreamCfg<D, ES, G>::NW * 32, kCtasPerSm)
                     for (int j = 0; j < 2; ++j) {
                         const int h = 8 * t + 2 * tig + j;
                         const float sc_out = l[t][j] > 0.f ? unit_v_scale(a, w.hk) / l[t][j] : 0.f;
+                        if constexpr (WS)
+                            if (h < G && gid == 0)
+                                a.softmax[static_cast<int64_t>(w.b) * a.num_q_heads + w.hk * G + h] = make_float2(m[t][j], 1.f / l[t][j]);
                         if (h < G) {
 #pragma unroll
                             for (int mt = 0; mt < Gm::MT; ++mt) {
@@ -1059,7 +1085,7 @@ __global__ void __launch_bounds__(StreamCfg<D, ES, G>::NW * 32, kCtasPerSm)
     __syncthreads();
     const int nm = mlist[0];
     for (int i = 0; i < nm; ++i)
-        merge_unit<D, G, NW * 32, NW * R * Gm::SB + Sc::NBUF * Gm::XW * 32 * static_cast<int>(sizeof(float))>(
+        merge_unit<D, G, NW * 32, NW * R * Gm::SB + Sc::NBUF * Gm::XW * 32 * static_cast<int>(sizeof(float)), WS>(
             a, mlist[1 + 3 * i], mlist[2 + 3 * i], mlist[3 + 3 * i], tid, rings);
 }
 
@@ -1073,7 +1099,7 @@ __global__ void __launch_bounds__(StreamCfg<D, ES, G>::NW * 32, kCtasPerSm)
 template <int D>
 __host__ __device__ constexpr int merge_threads() { return 4 * D; }
 
-template <int D, int G>
+template <int D, int G, bool WS = false>
 __global__ void __launch_bounds__(merge_threads<D>()) merge_kernel(const DecodeArgs a) {
     constexpr int kMergeThreads = merge_threads<D>();
     constexpr int NG = D / 4;                // float4 groups per head: 16, 32, 64
@@ -1177,6 +1203,8 @@ __global__ void __launch_bounds__(merge_threads<D>()) merge_kernel(const DecodeA
         Lt += f * sm_l[j][g4];
     }
     const float sc_out = Lt > 0.f ? unit_v_scale(a, hk) / Lt : 0.f;
+    if constexpr (WS)
+        if (g4 == 0) a.softmax[static_cast<int64_t>(b) * a.num_q_heads + hk * G + h] = make_float2(Mt, 1.f / Lt);
     uint16_t* out = a.out + (static_cast<int64_t>(b) * a.num_q_heads + hk * G + h) * D;
     const uint32_t lo2 = f32_to_bf16(o.x * sc_out) | (static_cast<uint32_t>(f32_to_bf16(o.y * sc_out)) << 16);
     const uint32_t hi2 = f32_to_bf16(o.z * sc_out) | (static_cast<uint32_t>(f32_to_bf16(o.w * sc_out)) << 16);
@@ -1185,7 +1213,7 @@ __global__ void __launch_bounds__(merge_threads<D>()) merge_kernel(const DecodeA
 
 // ---------------------------------------------------------------- launch
 
-template <int D, int G, int ES = 1, bool E5M2 = false, bool BS = false>
+template <int D, int G, int ES = 1, bool E5M2 = false, bool BS = false, bool WS = false>
 cudaError_t launch_stream(const DecodeArgs& a, int ctas, cudaStream_t stream) {
     static_assert(stream_smem_bytes<D, ES, G, BS>() <= kSmemPerCta, "two CTAs must fit on one SM");
     static std::atomic<uint64_t> done_mask{0};
@@ -1194,7 +1222,7 @@ cudaError_t launch_stream(const DecodeArgs& a, int ctas, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
     if (bit == 0 || !(done_mask.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(stream_decode_kernel<D, G, ES, E5M2, BS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(stream_decode_kernel<D, G, ES, E5M2, BS, WS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(stream_smem_bytes<D, ES, G, BS>()));
         if (e != cudaSuccess) return e;
         done_mask.fetch_or(bit, std::memory_order_release);
@@ -1209,7 +1237,7 @@ cudaError_t launch_stream(const DecodeArgs& a, int ctas, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, stream_decode_kernel<D, G, ES, E5M2, BS>, a);
+    e = cudaLaunchKernelEx(&cfg, stream_decode_kernel<D, G, ES, E5M2, BS, WS>, a);
     if (e != cudaSuccess || ctas == 1 || a.inline_merge) return e;  // merged inside the decode grid
     cudaLaunchConfig_t mcfg = {};
     mcfg.gridDim = dim3(a.batch * a.num_kv_heads, G);
@@ -1218,18 +1246,18 @@ cudaError_t launch_stream(const DecodeArgs& a, int ctas, cudaStream_t stream) {
     mcfg.stream = stream;
     mcfg.attrs = attr;
     mcfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&mcfg, merge_kernel<D, G>, a);
+    return cudaLaunchKernelEx(&mcfg, merge_kernel<D, G, WS>, a);
 }
 
-template <int D, int ES = 1, bool E5M2 = false, bool BS = false>
+template <int D, int ES = 1, bool E5M2 = false, bool BS = false, bool WS = false>
 cudaError_t launch_stream_g(int G, const DecodeArgs& a, int ctas, cudaStream_t s) {
     switch (G) {
-        case 1: return launch_stream<D, 1, ES, E5M2, BS>(a, ctas, s);
-        case 2: return launch_stream<D, 2, ES, E5M2, BS>(a, ctas, s);
-        case 4: return launch_stream<D, 4, ES, E5M2, BS>(a, ctas, s);
-        case 8: return launch_stream<D, 8, ES, E5M2, BS>(a, ctas, s);
+        case 1: return launch_stream<D, 1, ES, E5M2, BS, WS>(a, ctas, s);
+        case 2: return launch_stream<D, 2, ES, E5M2, BS, WS>(a, ctas, s);
+        case 4: return launch_stream<D, 4, ES, E5M2, BS, WS>(a, ctas, s);
+        case 8: return launch_stream<D, 8, ES, E5M2, BS, WS>(a, ctas, s);
         case 16:
-            if constexpr (D <= 128) return launch_stream<D, 16, ES, E5M2, BS>(a, ctas, s);
+            if constexpr (D <= 128) return launch_stream<D, 16, ES, E5M2, BS, WS>(a, ctas, s);
             else return cudaErrorInvalidValue;  // g = 16 at d = 256 runs as two units of 8 (head_map)
         default: return cudaErrorInvalidValue;
     }
@@ -1237,5 +1265,8 @@ cudaError_t launch_stream_g(int G, const DecodeArgs& a, int ctas, cudaStream_t s
 
 // The decode over a block-scaled cache (paged_decode_block.cu).
 cudaError_t launch_stream_block(int head_dim, int G, const DecodeArgs& a, int ctas, cudaStream_t s);
+
+// The decode that writes its scores, and the sums of weights after it (paged_decode_weights.cu).
+cudaError_t launch_stream_weights(int head_dim, int G, int es, bool e5m2, const DecodeArgs& a, int ctas, cudaStream_t s);
 
 }  // namespace fp8kv

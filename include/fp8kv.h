@@ -693,6 +693,43 @@ fp8kv_status fp8kv_tree_commit(void* k_cache, void* v_cache, int64_t num_blocks,
                                size_t workspace_bytes, void* stream);
 
 /*
+ * A decode step that keeps account of attention, for caches that evict by it
+ * (fp8kv_evict).  The output is that of the decode call of this cache format
+ * (fp8kv_paged_decode, _per_head, _e5m2, _bf16), bit for bit.  Beside it, for every kv
+ * head hk and attended token t of sequence b, with p_h(t) the probabilities that
+ * sum to 1 over the attended tokens for each of the g query heads h of hk:
+ *     weights[page(t)][hk][t % bs] = old(t) * decay + sum_h p_h(t)
+ * in fp32; old is what was there, but 0 for the newest token, t = L - 1, whose
+ * place may hold an earlier page's.  Tokens outside the window, and places past
+ * the sequence, are left as they are.  Nothing depends on the order of atomics:
+ * the same call gives the same bits.
+ *
+ *   weights        fp32 [num_blocks][num_kv_heads][block_size], 16-byte aligned.
+ *                  Zero-fill what a prompt's tokens occupy before the first
+ *                  call; a page in two sequences gets one of their sums.
+ *   decay          finite, >= 0: 1 adds up, less forgets
+ *   cache_format, k_scale, v_scale, k_scales, v_scales
+ *                  as fp8kv_paged_tree_attention
+ *   workspace      >= fp8kv_paged_decode_weights_workspace_size(...) bytes (the
+ *                  scores of up to 64 MiB, or of one sequence), otherwise as
+ *                  fp8kv_paged_decode.  The weights of a page whose block id is out
+ *                  of range are not written.
+ *   all other arguments, the shapes supported and the errors as fp8kv_paged_decode
+ */
+fp8kv_status fp8kv_paged_decode_weights(const void* q, const void* k_cache, const void* v_cache, int64_t num_blocks,
+                                        const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                        int max_seq_len, int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                                        int block_size, int cache_format, float k_scale, float v_scale,
+                                        const float* k_scales, const float* v_scales, float sm_scale, int window,
+                                        void* out, float* weights, float decay, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of fp8kv_paged_decode_weights on the CURRENT device; 0 if the
+ * arguments are invalid or no device is available. */
+size_t fp8kv_paged_decode_weights_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                                                 int max_seq_len, int block_size, int window);
+
+/*
  * Cuts every sequence back to `budget` tokens by accumulated attention weight,
  * each kv head for itself (a page holds one head's rows, so heads may keep
  * different tokens).  Of sequence b's L = seq_lens[b] tokens, where L > budget, kv
@@ -704,7 +741,8 @@ fp8kv_status fp8kv_tree_commit(void* k_cache, void* v_cache, int64_t num_blocks,
  * nothing moves.  Keys keep the rotation of their old position: later tokens are
  * rotated by their true positions, not by their place.
  *
- *   weights        fp32 [num_blocks][num_kv_heads][block_size], 16-byte aligned
+ *   weights        fp32 [num_blocks][num_kv_heads][block_size], 16-byte aligned,
+ *                  as fp8kv_paged_decode_weights keeps them
  *   budget         >= 1; sinks >= 0, recent >= 0, sinks + recent <= budget
  *   new_lens       int32 [batch] on the device, written: min(L, budget).  Not
  *                  seq_lens itself.

@@ -1,4 +1,4 @@
-"""Drafted trees and eviction without a GPU: the C ABI refuses bad arguments before it touches the device, the binding refuses
+"""Drafted trees, attention weights and eviction without a GPU: the C ABI refuses bad arguments before it touches the device, the binding refuses
 shapes that do not fit and tensors that are not on one, and the cut of a tree's work over CTAs is whole."""
 import ctypes
 import os
@@ -197,3 +197,33 @@ def test_binding_refuses_what_commit_and_evict_cannot_take():
         fk.fp8kv_evict(**ok)
     with pytest.raises(ValueError):
         fk.fp8kv_evict(**{**ok, "kept": i32(2, 2, 9)})
+
+
+def _weights(lib, **kw):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, nb=100, bt=FAKE, mb=8, sl=FAKE, msl=128, B=2, hq=32, hkv=8, d=128, bs=16, fmt=0, ks=0.5,
+             vs=0.5, hk=None, hv=None, sm=0.1, win=0, out=FAKE, w=FAKE, decay=0.9, ws=FAKE, wsb=1 << 20)
+    a.update(kw)
+    return lib.fp8kv_paged_decode_weights(
+        a["q"], a["k"], a["v"], a["nb"], a["bt"], a["mb"], a["sl"], a["msl"], a["B"], a["hq"], a["hkv"], a["d"], a["bs"],
+        a["fmt"], a["ks"], a["vs"], a["hk"], a["hv"], a["sm"], a["win"], a["out"], a["w"], a["decay"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw,code", SHAPES + SCALED + [
+    (dict(w=None), 1), (dict(w=OFF4), 1), (dict(decay=-0.1), 1), (dict(decay=float("nan")), 1),
+    (dict(decay=float("inf")), 1), (dict(B=0, q=None, out=None, w=None), 0),
+])
+def test_decode_weights_validates(lib, kw, code):
+    assert _weights(lib, **kw) == code
+
+
+def test_binding_refuses_what_the_weights_cannot_take():
+    q = torch.zeros((2, 8, 64), dtype=torch.bfloat16)
+    cache, ws = torch.zeros((3, 2, 16, 64), dtype=torch.uint8), torch.zeros(256, dtype=torch.uint8)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    ok = dict(q=q, k_cache=cache, v_cache=cache, block_tables=i32(2, 3), seq_lens=i32(2), max_seq_len=40, sm_scale=0.1,
+              window=0, out=q, weights=torch.zeros((3, 2, 16)), decay=1.0, workspace=ws)
+    with pytest.raises(TypeError):
+        fk.fp8kv_paged_decode_weights(**ok)
+    for bad in (dict(out=q[:1]), dict(seq_lens=i32(3))):
+        with pytest.raises(ValueError):
+            fk.fp8kv_paged_decode_weights(**{**ok, **bad})
