@@ -100,7 +100,7 @@ int main() {
                 if (lo < 0) lo = 0;
                 if (first_key(L[b], n[b], window) != lo || np != (L[b] - 1) / 16 - lo / 16 + 1) return 1;
             } else if (np != 0) return 2;
-            pre[b + 1] = pre[b] + static_cast<int64_t>(np) * H * blocks[b];
+            pre[b + 1] = pre[b] + static_cast<int64_t>(np + kLeadPages) * H * blocks[b];
         }
         const int64_t P = pre[B];
         if (P == 0) continue;
@@ -110,25 +110,35 @@ int main() {
         std::vector<int> got(P, 0);
         std::vector<int> slots(2 * C, 0);
         for (int c = 0; c < C; ++c) {
-            const int64_t e = range_start(part, c + 1);
-            for (int64_t pos = range_start(part, c); pos < e;) {
-                const Segment s = segment_at(pos, e, pre.data(), B, H, [&](int b) { return blocks[b]; });
+            const int64_t r0 = range_start(part, c), e = range_start(part, c + 1);
+            for (int64_t pos = r0; pos < e;) {
+                const Segment s = segment_at(pos, e, pre.data(), B, [&](int b) { return blocks[b]; },
+                                             [&](int b) { return unit_pages(L[b], n[b], window); });
                 const int np = unit_pages(L[s.b], n[s.b], window);
                 if (s.np != np || s.hk < 0 || s.hk >= H || s.rb < 0 || s.rb >= blocks[s.b]) return 4;
-                if (s.base != pre[s.b] + (static_cast<int64_t>(s.hk) * blocks[s.b] + s.rb) * np) return 5;
-                if (s.lp0 < 0 || s.lp1 <= s.lp0 || s.lp1 > np) return 6;
-                for (int p = s.lp0; p < s.lp1; ++p) ++got[s.base + p];
-                const int c0 = cta_of(part, s.base), c1 = cta_of(part, s.base + np - 1);
+                if (s.base != pre[s.b] + (static_cast<int64_t>(s.hk) * blocks[s.b] + s.rb) * (np + kLeadPages)) return 5;
+                if (s.lp0 < 0 || s.lp1 < s.lp0 || s.lp1 > np) return 6;
+                pos = unit_end(s);
+                if (s.lp0 == s.lp1) {
+                    if (pos < e) return 10;      // only where the range ends in a lead
+                    continue;
+                }
+                for (int p = s.lp0; p < s.lp1; ++p) ++got[s.base + kLeadPages + p];
+                const int c0 = cta_of(part, s.base + kLeadPages), c1 = cta_of(part, s.base + kLeadPages + np - 1);
                 if ((c0 == c1) != (s.lp0 == 0 && s.lp1 == np) || c < c0 || c > c1) return 7;
                 if (c0 != c1) {
                     const int64_t slot = partial_slot(part, c, s.base);
-                    if (slot < 2 * c || slot > 2 * c + 1 || slots[slot]++) return 8;
+                    if (slot != 2 * c + (c == c0) || slots[slot]++) return 8;
                 }
-                pos = s.base + s.lp1;
             }
         }
-        for (int64_t p = 0; p < P; ++p)
-            if (got[p] != 1) return 9;
+        for (int b = 0; b < B; ++b)
+            for (int u = 0; u < H * blocks[b]; ++u) {
+                const int np = unit_pages(L[b], n[b], window);
+                const int64_t base = pre[b] + static_cast<int64_t>(u) * (np + kLeadPages);
+                for (int64_t p = 0; p < kLeadPages + np; ++p)
+                    if (got[base + p] != (p >= kLeadPages)) return 9;
+            }
     }
     return 0;
 }
