@@ -132,7 +132,8 @@ __global__ void __launch_bounds__(256) commit_kernel(const Args a) {
 
 constexpr int kEvictThreads = 512;
 constexpr int kBins = 2048;
-constexpr int kChunks = 8;        // 16-byte chunks a thread holds in a round
+constexpr int kChunks = 4;        // 16-byte chunks a thread moves in a round
+constexpr int kStage = kEvictThreads * kChunks * 16;   // bytes of a CTA's round
 
 // A weight as a key whose unsigned order is the weights': -0 is 0, a NaN is below all.
 __device__ __forceinline__ uint32_t key_of(float w) {
@@ -164,20 +165,26 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
     return before + x - v;
 }
 
+// Words of the keys' place: they make way for two rounds of rows.
+__host__ __device__ constexpr int keys_words(int per_cta) { return per_cta > kStage / 2 ? per_cta : kStage / 2; }
+
 // One cluster per (kv head, sequence).  CTA r of it holds tokens
 // [r * per_cta, (r + 1) * per_cta) of the sequence as keys, later their kept ones
 // as a list of offsets.
 template <int RB>
 __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const Args a) {
     cg::cluster_group cluster = cg::this_cluster();
-    extern __shared__ __align__(16) uint32_t keys[];     // [per_cta], then uint16 list[per_cta]
+    extern __shared__ __align__(16) uint32_t keys[];     // [per_cta], later two rounds' rows; then uint16 list[per_cta]
     __shared__ __align__(16) int hist[kBins];
     __shared__ int warp_sums[kEvictThreads / 32];
     __shared__ int found[2];                             // a pass's digit, and how many of its tokens stay
     __shared__ int counts[2];                            // this CTA's ties, and tokens that stay for sure
     __shared__ int place[17];                            // first kept place of each CTA's list; budget
-    constexpr int CPR = RB / 16;
-    uint16_t* list = reinterpret_cast<uint16_t*>(keys + a.per_cta);
+    constexpr int CPR = RB / 16, ROW = 2 * CPR;          // chunks of a row: K's, with V's
+    constexpr int RUN = kEvictThreads * kChunks / ROW;   // rows a CTA moves in a round
+    static_assert(RUN <= kEvictThreads, "a thread looks up at most one row a round");
+    __shared__ int64_t from[4][RUN], to[4][RUN];         // of round k in [k & 3]
+    uint16_t* list = reinterpret_cast<uint16_t*>(keys + keys_words(a.per_cta));
     const int tid = threadIdx.x, rank = static_cast<int>(cluster.block_rank()), size = static_cast<int>(cluster.num_blocks());
     const int hk = blockIdx.x / size, b = blockIdx.y;
     griddep_wait();
@@ -298,54 +305,66 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const Args a) {
     if (kept)
         for (int i = tid; i < place[rank + 1] - place[rank]; i += kEvictThreads) kept[place[rank] + i] = t0 + list[i];
 
-    // ---- the rows, in rounds of the whole cluster: read a run, meet, write it.
-    // (The next round's reads need not wait for these writes: see the top.)
-    constexpr int ROW = 2 * CPR;                         // chunks of a row, K's and V's
-    constexpr int RUN = kEvictThreads * kChunks / ROW;   // rows a CTA moves in a round
-    static_assert(RUN <= kEvictThreads, "a thread moves at most one weight a round");
-    // where kept row i lies
-    auto source = [&](int i) {
-        int r = 0;
-        while (i >= place[r + 1]) ++r;
-        return r * a.per_cta + cluster.map_shared_rank(list, r)[i - place[r]];
-    };
-    for (int r0 = 0; r0 < a.budget; r0 += size * RUN) {
-        const int first = r0 + rank * RUN;
-        uint4 x[kChunks];
-        uint8_t* to[kChunks];
+    // ---- the rows, in rounds of the whole cluster: a round is read while the one
+    // before it is written (see the top), and its rows' places are looked up a
+    // round earlier still.
+    // rows of this CTA's run of round k, a thread each: where they lie, where they go, their weight
+    const int rounds = (a.budget + size * RUN - 1) / (size * RUN);
+    auto look_up = [&](int k) {
         float w = 0.f;
-        float* wto = nullptr;
-#pragma unroll
-        for (int j = 0; j < kChunks; ++j) {
-            const int c = j * kEvictThreads + tid, i = first + c / ROW, part = c % ROW;
-            to[j] = nullptr;
+        if (tid < RUN) {
+            const int i = (k * size + rank) * RUN + tid;
+            int64_t f = -1, t = 0;
             if (i < a.budget) {
-                const int src = source(i);
+                int r = 0;
+                while (i >= place[r + 1]) ++r;
+                const int src = r * a.per_cta + cluster.map_shared_rank(list, r)[i - place[r]];
                 if (src != i) {
                     const int bs = block_of(a, table, src), bd = block_of(a, table, i);
                     if (bs >= 0 && bd >= 0) {
-                        uint8_t* cache = (part < CPR ? a.k_cache : a.v_cache) + (part % CPR) * 16;
-                        x[j] = ld_input(reinterpret_cast<const uint4*>(cache + row_at(a, bs, hk, src) * RB));
-                        to[j] = cache + row_at(a, bd, hk, i) * RB;
+                        f = row_at(a, bs, hk, src);
+                        t = row_at(a, bd, hk, i);
+                        w = ld_input(a.weights + f);
                     }
                 }
             }
+            from[k & 3][tid] = f;
+            to[k & 3][tid] = t;
         }
-        if (tid < RUN && first + tid < a.budget) {
-            const int i = first + tid, src = source(i);
-            if (src != i) {
-                const int bs = block_of(a, table, src), bd = block_of(a, table, i);
-                if (bs >= 0 && bd >= 0) {
-                    w = ld_input(a.weights + row_at(a, bs, hk, src));
-                    wto = a.weights + row_at(a, bd, hk, i);
-                }
-            }
-        }
-        cluster.sync();                                  // the round is read
+        return w;
+    };
+    // Chunk j of the thread is chunk (j * threads + tid) of the run, K's and V's of a
+    // row beside each other; the thread that stages a chunk writes it.
+    const uint32_t stage = smem_u32(keys);               // (the keys are done with)
+    auto read = [&](int k) {
 #pragma unroll
-        for (int j = 0; j < kChunks; ++j)
-            if (to[j]) *reinterpret_cast<uint4*>(to[j]) = x[j];
-        if (wto) *wto = w;
+        for (int j = 0; j < kChunks; ++j) {
+            const int c = j * kEvictThreads + tid, part = c % ROW;
+            const int64_t f = from[k & 3][c / ROW];
+            if (f >= 0)
+                cp_async_16(stage + (k & 1) * kStage + c * 16,
+                            (part < CPR ? a.k_cache : a.v_cache) + f * RB + (part % CPR) * 16);
+        }
+        cp_async_commit();
+    };
+    float w = look_up(0), w1 = look_up(1);
+    __syncthreads();
+    read(0);
+    for (int k = 0; k < rounds; ++k) {
+        if (k + 1 < rounds) read(k + 1); else cp_async_commit();
+        const float w2 = k + 2 < rounds ? look_up(k + 2) : 0.f;
+        cp_async_wait<1>();
+        cluster.sync();                                  // round k is read
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) {
+            const int c = j * kEvictThreads + tid, part = c % ROW, i = c / ROW;
+            if (from[k & 3][i] >= 0)
+                *reinterpret_cast<uint4*>((part < CPR ? a.k_cache : a.v_cache) + to[k & 3][i] * RB + (part % CPR) * 16) =
+                    *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(keys) + (k & 1) * kStage + c * 16);
+        }
+        if (tid < RUN && from[k & 3][tid] >= 0) a.weights[to[k & 3][tid]] = w;
+        w = w1;
+        w1 = w2;
     }
     cluster.sync();                                      // no CTA leaves while its list is read
 }
@@ -354,6 +373,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const Args a) {
 
 constexpr int kMaxCluster = 16;
 constexpr int kMaxPerCta = 24576;   // tokens a CTA holds at most: 6 bytes each, 144 KB
+
+int evict_smem(int per_cta) { return keys_words(per_cta) * 4 + per_cta * 2; }
 
 template <typename Kernel>
 static cudaError_t launch(Kernel kernel, dim3 grid, int threads, int smem, int cluster, const Args& a, cudaStream_t s) {
@@ -382,7 +403,7 @@ static cudaError_t launch_evict(const Args& a, int cluster, int smem, cudaStream
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
     if (bit == 0 || !(done_mask.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(evict_kernel<RB>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxPerCta * 6);
+        e = cudaFuncSetAttribute(evict_kernel<RB>, cudaFuncAttributeMaxDynamicSharedMemorySize, evict_smem(kMaxPerCta));
         if (e == cudaSuccess) e = cudaFuncSetAttribute(evict_kernel<RB>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         done_mask.fetch_or(bit, std::memory_order_release);
@@ -495,7 +516,7 @@ extern "C" fp8kv_status fp8kv_evict(void* k_cache, void* v_cache, float* weights
     a.sinks = sinks;
     a.recent = recent;
     a.per_cta = per_cta(cluster);
-    const int smem = std::max(a.per_cta * 6, 16);
+    const int smem = evict_smem(a.per_cta);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int rb = head_dim * (cache_format == FP8KV_CACHE_BF16 ? 2 : 1);
     const cudaError_t e = rb == 64    ? launch_evict<64>(a, cluster, smem, s)
