@@ -175,7 +175,7 @@ template <int RB>
 __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const Args a) {
     cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ __align__(16) uint32_t keys[];     // [per_cta], later two rounds' rows; then uint16 list[per_cta]
-    __shared__ __align__(16) int hist[kBins];
+    __shared__ __align__(16) int hist[kBins], counted[kBins], sums[kBins];
     __shared__ int warp_sums[kEvictThreads / 32];
     __shared__ int found[2];                             // a pass's digit, and how many of its tokens stay
     __shared__ int counts[2];                            // this CTA's ties, and tokens that stay for sure
@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const Args a) {
     constexpr int CPR = RB / 16, ROW = 2 * CPR;          // chunks of a row: K's, with V's
     constexpr int RUN = kEvictThreads * kChunks / ROW;   // rows a CTA moves in a round
     static_assert(RUN <= kEvictThreads, "a thread looks up at most one row a round");
+    static_assert(kBins == 4 * kEvictThreads, "a thread has four bins");
     __shared__ int64_t from[4][RUN], to[4][RUN];         // of round k in [k & 3]
     uint16_t* list = reinterpret_cast<uint16_t*>(keys + keys_words(a.per_cta));
     const int tid = threadIdx.x, rank = static_cast<int>(cluster.block_rank()), size = static_cast<int>(cluster.num_blocks());
@@ -205,35 +206,78 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const Args a) {
     const int t0 = rank * a.per_cta, n = max(0, min(a.per_cta, L - t0));
     auto is_fixed = [&](int i) { return t0 + i < a.sinks || t0 + i >= L - a.recent; };
 
-    // ---- the keys (per_cta is a multiple of 16: four tokens lie in one page)
-    for (int i = tid * 4; i < n; i += kEvictThreads * 4) {
-        const int id = block_of(a, table, t0 + i);
-        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (id >= 0) w = ld_input(reinterpret_cast<const float4*>(a.weights + row_at(a, id, hk, t0 + i)));
-        *reinterpret_cast<uint4*>(keys + i) = make_uint4(key_of(w.x), key_of(w.y), key_of(w.z), key_of(w.w));
+    // ---- the keys (per_cta is a multiple of 16: four tokens lie in one page), and
+    // the first pass's counts
+    *reinterpret_cast<int4*>(hist + 4 * tid) = make_int4(0, 0, 0, 0);
+    __syncthreads();
+    constexpr int AT = 4;                                // reads of a thread at once
+    for (int i0 = tid * 4; i0 < n; i0 += kEvictThreads * 4 * AT) {
+        int id[AT];
+        float4 w[AT];
+#pragma unroll
+        for (int j = 0; j < AT; ++j) {
+            const int i = i0 + j * kEvictThreads * 4;
+            id[j] = i < n ? block_of(a, table, t0 + i) : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < AT; ++j) {
+            const int i = i0 + j * kEvictThreads * 4;
+            w[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (id[j] >= 0) w[j] = ld_input(reinterpret_cast<const float4*>(a.weights + row_at(a, id[j], hk, t0 + i)));
+        }
+#pragma unroll
+        for (int j = 0; j < AT; ++j) {
+            const int i = i0 + j * kEvictThreads * 4;
+            const uint32_t k[4] = {key_of(w[j].x), key_of(w[j].y), key_of(w[j].z), key_of(w[j].w)};
+            if (i >= n) break;
+            *reinterpret_cast<uint4*>(keys + i) = make_uint4(k[0], k[1], k[2], k[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < n && !is_fixed(i + e)) atomicAdd(&hist[k[e] >> 21], 1);
+        }
     }
     // ---- the smallest kept key, digit by digit: `want` of the tokens that are not fixed stay
     int want = a.budget - a.sinks - a.recent;
     uint32_t least = want > 0 ? 0u : ~0u;                // (no weight has the key ~0)
     if (want > 0) {
+        // Two CTAs read each other's counts.  More sum a share of the bins each, then
+        // all read the sums: 16 KB a CTA, where every count is 8 KB a CTA of the
+        // cluster (16 CTAs: a pass of 3 us, 8 us by reading every count; 2 CTAs: 2.4
+        // and 2.0 us).
+        const int nb = kBins / size;
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, mask = pass == 2 ? 1023 : 2047;
-            for (int i = tid; i < kBins; i += kEvictThreads) hist[i] = 0;
-            __syncthreads();                             // (and the keys are there)
-            for (int i = tid; i < n; i += kEvictThreads) {
-                const uint32_t k = keys[i];
-                if (!is_fixed(i) && (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == least)) atomicAdd(&hist[(k >> shift) & mask], 1);
+            if (pass > 0) {
+                *reinterpret_cast<int4*>(hist + 4 * tid) = make_int4(0, 0, 0, 0);
+                __syncthreads();
+                for (int i = tid; i < n; i += kEvictThreads) {
+                    const uint32_t k = keys[i];
+                    if ((k >> (pass == 1 ? 21 : 10)) == least && !is_fixed(i)) atomicAdd(&hist[(k >> shift) & mask], 1);
+                }
             }
-            cluster.sync();
-            // thread t sums bins 2047 - 4 t and the three below over the cluster
-            int c[4], all;
+            cluster.sync();                              // the counts are there
+            // thread t has bins 2047 - 4 t and the three below
+            int c[4] = {0, 0, 0, 0}, all;
             const int top = kBins - 1 - 4 * tid;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) c[j] = 0;
-            for (int r = 0; r < size; ++r) {
-                const int4 x = *reinterpret_cast<const int4*>(cluster.map_shared_rank(hist, r) + top - 3);
+            auto add = [&](const int* from) {
+                const int4 x = *reinterpret_cast<const int4*>(from);
                 c[0] += x.w; c[1] += x.z; c[2] += x.y; c[3] += x.x;
+            };
+            if (size <= 2) {
+                for (int r = 0; r < size; ++r) add(cluster.map_shared_rank(hist, r) + top - 3);
+                cluster.sync();                          // every count is read
+            } else {
+                *reinterpret_cast<int4*>(counted + 4 * tid) =
+                    *reinterpret_cast<const int4*>(cluster.map_shared_rank(hist, 4 * tid / nb) + rank * nb + 4 * tid % nb);
+                __syncthreads();
+                for (int i = tid; i < nb; i += kEvictThreads) {
+                    int x = 0;
+                    for (int r = 0; r < size; ++r) x += counted[r * nb + i];
+                    sums[i] = x;
+                }
+                cluster.sync();                          // every count is read, and the sums are there
+                add(cluster.map_shared_rank(sums, (top - 3) / nb) + (top - 3) % nb);
             }
             const int mine = (c[0] + c[1]) + (c[2] + c[3]);
             int above = block_scan(mine, warp_sums, all);
@@ -247,7 +291,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const Args a) {
                 found[0] = top - j;
                 found[1] = want - above;
             }
-            cluster.sync();                              // every CTA has read every count
+            __syncthreads();
             least = (least << (pass == 2 ? 10 : 11)) | static_cast<uint32_t>(found[0]);
             want = found[1];
         }
@@ -257,17 +301,18 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const Args a) {
     // Keys above `least` stay, and the first `want` of those equal to it.
     // ---- what of this CTA's tokens stays: each thread a run (of odd length: no bank conflicts)
     const int per = ((n + kEvictThreads - 1) / kEvictThreads) | 1, i0 = min(n, tid * per), i1 = min(n, i0 + per);
-    int ties = 0, sure = 0, all_ties, all_sure;
+    uint64_t ties = 0, sure = 0;                         // bits of the run
     for (int i = i0; i < i1; ++i) {
-        const bool f = is_fixed(i);
-        sure += f || keys[i] > least;
-        ties += !f && keys[i] == least;
+        const uint64_t bit = 1ull << (i - i0);
+        if (is_fixed(i) || keys[i] > least) sure |= bit;
+        else if (keys[i] == least) ties |= bit;
     }
-    const int ties_before = block_scan(ties, warp_sums, all_ties);
-    const int sure_before = block_scan(sure, warp_sums, all_sure);
+    int all;                                             // (two counts in one scan: each is below 2^16)
+    const int before_me = block_scan(__popcll(ties) | __popcll(sure) << 16, warp_sums, all);
+    const int ties_before = before_me & 0xFFFF, sure_before = before_me >> 16;
     if (tid == 0) {
-        counts[0] = all_ties;
-        counts[1] = all_sure;
+        counts[0] = all & 0xFFFF;
+        counts[1] = all >> 16;
     }
     cluster.sync();
     if (tid < 32) {
@@ -299,8 +344,10 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const Args a) {
     __syncthreads();
     const int ties_left = found[0];
     int at = sure_before + min(ties_left, ties_before), tie = ties_before;
-    for (int i = i0; i < i1; ++i)
-        if (is_fixed(i) || keys[i] > least || (keys[i] == least && tie++ < ties_left)) list[at++] = static_cast<uint16_t>(i);
+    for (uint64_t left = sure | ties; left; left &= left - 1) {
+        const uint64_t bit = left & (~left + 1);
+        if ((sure & bit) || tie++ < ties_left) list[at++] = static_cast<uint16_t>(i0 + __ffsll(static_cast<long long>(bit)) - 1);
+    }
     cluster.sync();                                      // the lists are there
     if (kept)
         for (int i = tid; i < place[rank + 1] - place[rank]; i += kEvictThreads) kept[place[rank] + i] = t0 + list[i];
@@ -372,7 +419,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const Args a) {
 // ---------------------------------------------------------------- host side
 
 constexpr int kMaxCluster = 16;
-constexpr int kMaxPerCta = 24576;   // tokens a CTA holds at most: 6 bytes each, 144 KB
+constexpr int kMaxPerCta = 24576;   // tokens a CTA holds at most: 6 bytes each, 144 KB; 48 a thread
 
 int evict_smem(int per_cta) { return keys_words(per_cta) * 4 + per_cta * 2; }
 
