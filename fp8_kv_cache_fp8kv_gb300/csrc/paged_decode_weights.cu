@@ -9,6 +9,9 @@
 //     weights_t = old_t decay + sum_h 2^(s_ht - m_h) / l_h,
 // one thread a token, so the sum has one order and the result one value.
 // Reading K again instead would cost d bytes a token (128, against 8 g = 32 at g = 4).
+// Measured (GB300, 8 x 20K, 32 over 8 heads of 128, E4M3): 74.1 us, 4.5 TB/s, of
+// which the second kernel about 10 (fp8kv_paged_decode alone 59.6); 1 x 4096 10.7 us
+// (9.2).  Four tokens a thread: 73.3 and 12.5 us.
 #include "stream_decode.cuh"
 
 namespace fp8kv {

@@ -28,6 +28,15 @@
 // Scores, the softmax and P.V accumulate in FP32.  The reference m_r of a row is a
 // whole number, moved only where 64 keys' weights grow too large for f16 (or at
 // masked keys), so scaling what was summed under another is exact.
+//
+// Measured (GB300, graph of calls, 32 over 8 heads of 128, E4M3): 8 x 20K tokens,
+// 16 nodes 84.6 us (3.9 TB/s, 501 TFLOP/s; tensor pipe 47% active), 12 to 80 nodes
+// of 64 at most 223 us (759 TFLOP/s, tensor pipe 56%), 128 nodes 357 us (950
+// TFLOP/s); 1 x 4096, 8 nodes 18.8 us.  What bounds it is the round of a stage,
+// S -> weights -> P V -> the next S of the same tile: of 3480 cycles (two tiles,
+// 128 keys) 2048 are MMAs.  Alone, no part of it sets the pace: without copies 214
+// us instead of 223, without the exponentials 219, without the conversion of V 216,
+// with one MMA of each product 190.
 #pragma once
 
 #include <cuda_runtime.h>
