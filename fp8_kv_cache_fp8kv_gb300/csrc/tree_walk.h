@@ -26,9 +26,10 @@
 namespace fp8kv {
 namespace tree {
 
-// A turn to another unit takes about five stages' time.  1 x 4096 tokens, 8 nodes:
-// 26.2 us without the lead (six of 129 CTAs had two units), 18.8 us with it; 8 x
-// 20K, 16 nodes: 87.6 and 84.6 us.
+// A turn to another unit takes about five stages' time.  Measured with 16, 24, 40,
+// 56 and 80: 16 x 20K tokens, d 256, 8 nodes 67.1, 65.2, 59.8, 60.7 and 61.2 us; 8 x
+// 20K, d 128, 16 nodes 86.6, 85.9, 84.9, 84.1 and 84.0; 5 x 9K in bf16 88.6, 89.6,
+// 90.4, 93.0 and 96.0.
 constexpr int kLeadPages = 40;
 
 // CTAs that share P places: at least min_pages each, at most `most`.
