@@ -30,6 +30,7 @@ __global__ void __launch_bounds__(256) add_weights_kernel(const DecodeArgs a) {
     int id = in ? ld_input(a.block_tables + static_cast<int64_t>(b) * a.max_blocks_per_seq + t / kBS) : -1;
     if (id >= a.num_blocks) id = -1;                                    // (the decode reports it)
     griddep_wait();
+    if (*reinterpret_cast<volatile uint32_t*>(a.err) == FP8KV_ERR_TIMEOUT) return;   // (the decode was skipped: no scores)
     if (base + blockIdx.x * 256 >= L) return;
     if (tid < G * U) soft[tid] = a.softmax[static_cast<int64_t>(b) * a.num_q_heads + hk * G * U + tid];
     __syncthreads();

@@ -624,7 +624,8 @@ fp8kv_status fp8kv_paged_prefill_block(const void* q, int64_t num_q_tokens, cons
  *   seq_lens       int32 [batch] on the device
  *   q_starts       int32 [batch + 1] on the device, non-decreasing
  *   parents        int32 [num_tokens] on the device
- *   max_nodes      host-side bound of the trees' sizes, at most 256
+ *   max_nodes      host-side bound of the trees' sizes, at most 256 and
+ *                  max_seq_len
  *   k_scale ..     as fp8kv_rope_append: per-tensor scales (1 for a bf16 cache),
  *   v_scales       or DEVICE fp32 [num_kv_heads] arrays in their place (null
  *                  for a bf16 cache)
@@ -713,7 +714,7 @@ fp8kv_status fp8kv_tree_commit(void* k_cache, void* v_cache, int64_t num_blocks,
  *   workspace      >= fp8kv_paged_decode_weights_workspace_size(...) bytes (the
  *                  scores of up to 64 MiB, or of one sequence), otherwise as
  *                  fp8kv_paged_decode.  The weights of a page whose block id is out
- *                  of range are not written.
+ *                  of range are not written, nor any after FP8KV_ERR_TIMEOUT.
  *   all other arguments, the shapes supported and the errors as fp8kv_paged_decode
  */
 fp8kv_status fp8kv_paged_decode_weights(const void* q, const void* k_cache, const void* v_cache, int64_t num_blocks,

@@ -206,6 +206,25 @@ def test_the_stall_hook_without_a_stall_is_the_plain_call():
     assert fk.fp8kv_read_error(ws) == 0 and torch.equal(out, good)
 
 
+def test_no_weights_are_added_after_a_timeout():
+    """The decode skips its work on a workspace whose error word says so, and the weights stay as they were."""
+    c = Cache([700, 80], 8, 128)
+    q = queries(2, 32, 128, 3)
+    ws = fk.alloc_weights_workspace(2, 32, 8, 128, 700)
+    w = torch.rand((c.blocks, 8, PAGE), generator=torch.Generator().manual_seed(1)).cuda()
+    before, out = w.clone(), torch.full_like(q, 123)
+    args = (q, c.k, c.v, c.tables, c.seq_lens, 700, 128 ** -0.5, 0, out, w, 0.9, ws)
+    ws[:4].view(torch.int32).fill_(5)
+    ws[256:].fill_(0x55)
+    fk.fp8kv_paged_decode_weights(*args, **c.kind_args())
+    torch.cuda.synchronize()
+    assert torch.all(out == 123) and torch.equal(w, before) and fk.fp8kv_read_error(ws) == 5
+    fk.fp8kv_workspace_init(ws)
+    fk.fp8kv_paged_decode_weights(*args, **c.kind_args())
+    torch.cuda.synchronize()
+    assert fk.fp8kv_read_error(ws) == 0 and not torch.equal(w, before)
+
+
 def test_another_stream():
     c = Cache([700, 80], 8, 128)
     trees, q = trees_of([20, 7]), queries(27, 32, 128, 3)
