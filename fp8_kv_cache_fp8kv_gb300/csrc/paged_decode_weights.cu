@@ -20,6 +20,7 @@ namespace fp8kv {
 template <int G, int U>
 __global__ void __launch_bounds__(256) add_weights_kernel(const DecodeArgs a) {
     __shared__ float2 soft[G * U];
+    __shared__ uint32_t err;
     const int tid = threadIdx.x, b = blockIdx.z, hk = blockIdx.y;
     const int Hc = a.num_kv_heads / U;
     griddep_launch_dependents();
@@ -30,11 +31,12 @@ __global__ void __launch_bounds__(256) add_weights_kernel(const DecodeArgs a) {
     int id = in ? ld_input(a.block_tables + static_cast<int64_t>(b) * a.max_blocks_per_seq + t / kBS) : -1;
     if (id >= a.num_blocks) id = -1;                                    // (the decode reports it)
     griddep_wait();
-    if (*reinterpret_cast<volatile uint32_t*>(a.err) == FP8KV_ERR_TIMEOUT) return;   // (the decode was skipped: no scores)
     if (base + blockIdx.x * 256 >= L) return;
+    // (one thread asks: every warp's read of the one word made the 8 x 20K call 5 us longer)
+    if (tid == 255) err = *reinterpret_cast<volatile uint32_t*>(a.err);
     if (tid < G * U) soft[tid] = a.softmax[static_cast<int64_t>(b) * a.num_q_heads + hk * G * U + tid];
     __syncthreads();
-    if (id < 0) return;
+    if (id < 0 || err == FP8KV_ERR_TIMEOUT) return;                     // (the decode was skipped: no scores)
     float* w = a.weights + (static_cast<int64_t>(id) * Hc + hk) * kBS + t % kBS;
     const float old = t == L - 1 ? 0.f : *w * a.decay;
     float sum = 0.f;
