@@ -1024,6 +1024,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const Args a, int block
     constexpr int AT = D == 256 ? 4 : 8; // partials read at once
     __shared__ int64_t red[2][8];
     __shared__ float2 ml[AT][32];
+    __shared__ bool timed_out;
     griddep_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, lg = a.log2_group;
     const int u = blockIdx.x, rb = u % blocks, hk = u / blocks % a.num_kv_heads, b = u / blocks / a.num_kv_heads;
@@ -1062,7 +1063,8 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const Args a, int block
         c1 = cta_of(part, base + np - 1);
     }
     griddep_wait();   // every block waits: this grid must not complete before the attention has
-    if (c0 == c1 || *reinterpret_cast<volatile uint32_t*>(a.err) == FP8KV_ERR_TIMEOUT) return;   // no rows, or written by its only CTA
+    if (c0 == c1) return;   // no rows, or written by its only CTA
+    if (tid == 0) timed_out = *reinterpret_cast<volatile uint32_t*>(a.err) == FP8KV_ERR_TIMEOUT;
     // c0 began the unit in its range's last segment, the others have it in their first (partial_slot)
     auto slot_of = [&](int c) { return 2 * static_cast<int64_t>(c) + (c == c0); };
     float M = -INFINITY, l = 0.f;
@@ -1105,7 +1107,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const Args a, int block
             }
         __syncthreads();
     }
-    if (r >= (s.n << lg)) return;
+    if (timed_out || r >= (s.n << lg)) return;   // (the loop has met once at least)
     const float vs = a.v_scales ? ld_input(a.v_scales + hk) : a.v_scale;
     const float so = l > 0.f ? vs / l : l;
     uint2* orow = reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(s.q0 + (r >> lg)) * a.num_q_heads + (hk << lg) +
