@@ -30,9 +30,9 @@
 // masked keys), so scaling what was summed under another is exact.
 //
 // Measured (GB300, graph of calls, 32 over 8 heads of 128, E4M3): 8 x 20K tokens,
-// 16 nodes 84.6 us (3.9 TB/s, 501 TFLOP/s; tensor pipe 47% active), 12 to 80 nodes
-// of 64 at most 223 us (759 TFLOP/s, tensor pipe 56%), 128 nodes 357 us (950
-// TFLOP/s); 1 x 4096, 8 nodes 18.8 us.  What bounds it is the round of a stage,
+// 12 to 20 nodes 84.3 us (3.9 TB/s, 503 TFLOP/s; tensor pipe 47% active), 48 to 80
+// nodes 223 us (760 TFLOP/s, tensor pipe 56%), 128 nodes 356 us (953 TFLOP/s); 1 x
+// 4096, 8 nodes 18.7 us.  What bounds it is the round of a stage,
 // S -> weights -> P V -> the next S of the same tile: of 3480 cycles (two tiles,
 // 128 keys) 2048 are MMAs.  Alone, no part of it sets the pace: without copies 214
 // us instead of 223, without the exponentials 219, without the conversion of V 216,
